@@ -20,6 +20,7 @@ STATUS = {0: "I8_OK", 1: "I8_ERR_INVALID_ARG", 2: "I8_ERR_UNSUPPORTED", 3: "I8_E
 # every symbol the header declares, with (restype, argtypes)
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
+_I32 = ctypes.c_int32
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
 _ST = ctypes.c_int
@@ -49,6 +50,23 @@ SIGNATURES = {
     "i8_bias_grad": (_ST, [_P, _I64, _I64, _P, _P]),
     "i8_dequantize_weight": (_ST, [_P, _P, _I64, _I64, _P, _P]),
     "i8_dequantize_weight_e4m3": (_ST, [_P, _P, _I64, _I64, _P, _P]),
+    "i8_block_quantize_act": (_ST, [_P, _I32, _I64, _I64, _P, _P, _P]),
+    "i8_block_quantize_weight": (_ST, [_P, _I32, _I64, _I64, _I64, _P, _P, _P]),
+    "i8_block_linear_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "i8_block_linear_forward": (_ST, [_P, _I32, _I64, _I64, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
+    "i8_block_linear_backward_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "i8_block_linear_backward": (_ST, [_P, _P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P,
+                                       _SZ, _P]),
+    "i8_route_experts": (_ST, [_P, _I32, _I64, _I64, _P, _I32, _I64, _I64, _I64, _I32, _F, _P,
+                               _P, _P]),
+    "i8_route_experts_backward": (_ST, [_P, _I32, _I64, _I64, _I32, _I64, _I32, _F, _P, _P, _P,
+                                        _P]),
+    "i8_experts_workspace_size": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "i8_experts_forward": (_ST, [_P, _I32, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P, _I64, _I64,
+                                 _P, _P, _P, _SZ, _P]),
+    "i8_experts_backward_workspace_size": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "i8_experts_backward": (_ST, [_P, _I32, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P, _I64, _I64,
+                                  _P, _P, _P, _P, _SZ, _P]),
     "i8_sync_status": (_ST, [_P]),
     "i8_set_profile_events": (_ST, [_P, _P]),
     "i8_selftest_bounded_wait": (_ST, [_I64, _P]),
@@ -353,6 +371,214 @@ def i8_dequantize_weight(CB, SCB, W, stream=None):
     import torch
     fn = "i8_dequantize_weight" if CB.dtype == torch.int8 else "i8_dequantize_weight_e4m3"
     _check(fn, getattr(load(), fn)(_ptr(CB), _ptr(SCB), N, K, _ptr(W), _stream(stream)))
+
+
+# ------------------------------------------------- block-scaled e4m3, routing, experts
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _dtype16(t, name):
+    """The header's code of a 16-bit floating-point tensor's type."""
+    import torch
+    if t is not None and t.dtype == torch.float16:
+        return 0
+    if t is not None and t.dtype == torch.bfloat16:
+        return 1
+    raise TypeError("%s: dtype %s, expected torch.float16 or torch.bfloat16"
+                    % (name, None if t is None else t.dtype))
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def _codes():
+    return _dt("uint8", "float8_e4m3fn")
+
+
+def _bytes(t):
+    return t.numel() * t.element_size()
+
+
+def i8_block_quantize_act(X, Xq, SX, stream=None):
+    """Xq[T, K] e4m3 codes and SX[ceil(K/128), T] scales of X in row blocks of 128."""
+    code = _dtype16(X, "X")
+    T, K = _mat(X, "X", (X.dtype,))
+    _arg(Xq, "Xq", _codes(), T * K)
+    _arg(SX, "SX", _dt("float32"), _blocks(K) * T)
+    _check("i8_block_quantize_act",
+           load().i8_block_quantize_act(_ptr(X), code, T, K, _ptr(Xq), _ptr(SX),
+                                        _stream(stream)))
+
+
+def i8_block_quantize_weight(W, CB, SCB, stream=None):
+    """CB e4m3 codes and SCB scales of W ([N, K], or [..., N, K]: one weight after another) in
+    tiles of 128 x 128."""
+    code = _dtype16(W, "W")
+    if W.dim() < 2:
+        raise ValueError("W: a tensor of at least 2 dimensions is required")
+    N, K = W.shape[-2:]
+    Z = W.numel() // (N * K) if N * K else 0
+    _arg(CB, "CB", _codes(), Z * N * K)
+    _arg(SCB, "SCB", _dt("float32"), Z * _blocks(N) * _blocks(K))
+    _check("i8_block_quantize_weight",
+           load().i8_block_quantize_weight(_ptr(W), code, Z, N, K, _ptr(CB), _ptr(SCB),
+                                           _stream(stream)))
+
+
+def i8_block_linear_workspace_size(T, N, K) -> int:
+    return int(load().i8_block_linear_workspace_size(T, N, K))
+
+
+def _check_block_weight(CB, SCB, K, what):
+    N, Kc = _mat(CB, "CB", _codes())
+    if Kc != K:
+        raise ValueError("CB has %d columns, %s has %d" % (Kc, what, K))
+    _arg(SCB, "SCB", _dt("float32"), _blocks(N) * _blocks(K))
+    return N
+
+
+def i8_block_linear_forward(X, CB, SCB, bias, Y, workspace, stream=None):
+    """Y[T, N] = X W^T + bias with block-scaled e4m3 codes."""
+    code = _dtype16(X, "X")
+    T, K = _mat(X, "X", (X.dtype,))
+    N = _check_block_weight(CB, SCB, K, "X")
+    if bias is not None:
+        _arg(bias, "bias", (X.dtype,), N)
+    _arg(Y, "Y", (X.dtype,), T * N)
+    _check("i8_block_linear_forward",
+           load().i8_block_linear_forward(_ptr(X), code, T, K, _ptr(CB), _ptr(SCB), _ptr(bias),
+                                          N, _ptr(Y), _ptr(workspace), _bytes(workspace),
+                                          _stream(stream)))
+
+
+def i8_block_linear_backward_workspace_size(T, N, K) -> int:
+    return int(load().i8_block_linear_backward_workspace_size(T, N, K))
+
+
+def i8_block_linear_backward(dY, X, CB, SCB, dX, dW, db, workspace, stream=None):
+    """dX = q(dY) W' (needs CB, SCB), dW = t(dY)^T t(X) (needs X), db = sum of dY's rows; the
+    outputs that are None are left out."""
+    code = _dtype16(dY, "dY")
+    T, N = _mat(dY, "dY", (dY.dtype,))
+    if dX is not None:
+        K = _mat(dX, "dX", (dY.dtype,))[1]
+        _arg(dX, "dX", (dY.dtype,), T * K)
+        if _check_block_weight(CB, SCB, K, "dX") != N:
+            raise ValueError("CB has %d rows, dY has %d columns" % (CB.shape[0], N))
+    if dW is not None:
+        Tx, Kx = _mat(X, "X", (dY.dtype,))
+        if Tx != T:
+            raise ValueError("X has %d rows, dY has %d" % (Tx, T))
+        if dX is not None and Kx != K:
+            raise ValueError("X has %d columns, dX has %d" % (Kx, K))
+        K = Kx
+        _arg(dW, "dW", (dY.dtype,), N * K)
+    if dX is None and dW is None:
+        K = 16                              # no product: any valid width
+    if db is not None:
+        _arg(db, "db", (dY.dtype,), N)
+    _check("i8_block_linear_backward",
+           load().i8_block_linear_backward(
+               _ptr(dY), _ptr(X) if dW is not None else None, code, T, N, K,
+               _ptr(CB) if dX is not None else None, _ptr(SCB) if dX is not None else None,
+               _ptr(dX), _ptr(dW), _ptr(db), _ptr(workspace), _bytes(workspace),
+               _stream(stream)))
+
+
+def _logits(t):
+    import torch
+    if t is not None and t.dtype == torch.float32:
+        return 2
+    try:
+        return _dtype16(t, "logits")
+    except TypeError:
+        raise TypeError("logits: dtype %s, expected torch.float32, torch.float16 or "
+                        "torch.bfloat16" % (None if t is None else t.dtype)) from None
+
+
+def i8_route_experts(logits, balance, score, n_groups, top_groups, k, renormalize, scale,
+                     weights, idx, stream=None):
+    """weights[T, k] fp32 and idx[T, k] int32 of each token's experts; score: "softmax" or
+    "sigmoid"."""
+    code = _logits(logits)
+    T, E = _mat(logits, "logits", (logits.dtype,))
+    if balance is not None:
+        _arg(balance, "balance", _dt("float32"), E)
+    _arg(weights, "weights", _dt("float32"), T * k)
+    _arg(idx, "idx", _dt("int32"), T * k)
+    _check("i8_route_experts",
+           load().i8_route_experts(_ptr(logits), code, T, E, _ptr(balance), SCORES[score],
+                                   n_groups, top_groups, k, int(bool(renormalize)),
+                                   float(scale), _ptr(weights), _ptr(idx), _stream(stream)))
+
+
+def i8_route_experts_backward(logits, score, renormalize, scale, idx, dweights, dlogits,
+                              stream=None):
+    """dlogits[T, E] of i8_route_experts from dweights[T, k] and its idx[T, k]."""
+    code = _logits(logits)
+    T, E = _mat(logits, "logits", (logits.dtype,))
+    k = _mat(idx, "idx", _dt("int32"))[1]
+    _arg(idx, "idx", _dt("int32"), T * k)
+    _arg(dweights, "dweights", _dt("float32"), T * k)
+    _arg(dlogits, "dlogits", (logits.dtype,), T * E)
+    _check("i8_route_experts_backward",
+           load().i8_route_experts_backward(_ptr(logits), code, T, E, SCORES[score], k,
+                                            int(bool(renormalize)), float(scale), _ptr(idx),
+                                            _ptr(dweights), _ptr(dlogits), _stream(stream)))
+
+
+def _check_experts(X, name, idx, weights, CB13, S13, CB2, S2):
+    code = _dtype16(X, name)
+    T, K = _mat(X, name, (X.dtype,))
+    k = _mat(idx, "idx", _dt("int32"))[1]
+    _arg(idx, "idx", _dt("int32"), T * k)
+    _arg(weights, "weights", _dt("float32"), T * k)
+    if CB13 is None or CB13.dim() != 4 or CB13.shape[1] != 2 or CB13.shape[3] != K:
+        raise ValueError("CB13: [E, 2, I, %d] codes are required" % K)
+    E, _, I, _ = CB13.shape
+    if CB2 is None or tuple(CB2.shape) != (E, K, I):
+        raise ValueError("CB2: [%d, %d, %d] codes are required" % (E, K, I))
+    _arg(CB13, "CB13", _codes(), E * 2 * I * K)
+    _arg(CB2, "CB2", _codes(), E * K * I)
+    _arg(S13, "S13", _dt("float32"), E * 2 * _blocks(I) * _blocks(K))
+    _arg(S2, "S2", _dt("float32"), E * _blocks(K) * _blocks(I))
+    return code, T, K, k, E, I
+
+
+def i8_experts_workspace_size(T, K, I, E, k) -> int:
+    return int(load().i8_experts_workspace_size(T, K, I, E, k))
+
+
+def i8_experts_forward(X, idx, weights, CB13, S13, CB2, S2, Y, GU, workspace, stream=None):
+    """Y[T, K]: each token through the experts idx[T, k], summed with weights[T, k]."""
+    code, T, K, k, E, I = _check_experts(X, "X", idx, weights, CB13, S13, CB2, S2)
+    _arg(Y, "Y", (X.dtype,), T * K)
+    if GU is not None:
+        _arg(GU, "GU", _dt("float32"), T * k * 2 * I)
+    _check("i8_experts_forward",
+           load().i8_experts_forward(_ptr(X), code, T, K, _ptr(idx), _ptr(weights), k,
+                                     _ptr(CB13), _ptr(S13), _ptr(CB2), _ptr(S2), E, I, _ptr(Y),
+                                     _ptr(GU), _ptr(workspace), _bytes(workspace),
+                                     _stream(stream)))
+
+
+def i8_experts_backward_workspace_size(T, K, I, E, k) -> int:
+    return int(load().i8_experts_backward_workspace_size(T, K, I, E, k))
+
+
+def i8_experts_backward(dY, idx, weights, CB13, S13, CB2, S2, GU, dX, dweights, workspace,
+                        stream=None):
+    """dX[T, K] and dweights[T, k] of i8_experts_forward; GU as that call wrote it."""
+    code, T, K, k, E, I = _check_experts(dY, "dY", idx, weights, CB13, S13, CB2, S2)
+    _arg(GU, "GU", _dt("float32"), T * k * 2 * I)
+    _arg(dX, "dX", (dY.dtype,), T * K)
+    _arg(dweights, "dweights", _dt("float32"), T * k)
+    _check("i8_experts_backward",
+           load().i8_experts_backward(_ptr(dY), code, T, K, _ptr(idx), _ptr(weights), k,
+                                      _ptr(CB13), _ptr(S13), _ptr(CB2), _ptr(S2), E, I,
+                                      _ptr(GU), _ptr(dX), _ptr(dweights), _ptr(workspace),
+                                      _bytes(workspace), _stream(stream)))
 
 
 def i8_sync_status(stream=None) -> int:

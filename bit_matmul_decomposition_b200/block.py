@@ -1,0 +1,254 @@
+"""Linear layers with block-scaled e4m3 codes: one fp32 scale for each 128 x 128 tile of the
+weight and for each 128 features of a token.
+
+Where ``Linear8bitLt`` keeps one scale per row and takes the outlier columns out into an fp16
+product, a block's scale confines an outlier to its block, so every feature goes through the
+8-bit product.  The weight format (e4m3 codes and a scale tensor of one entry per 128 x 128
+tile, value = code * scale) is that of checkpoints stored in it: ``LinearBlockFp8.from_codes``
+takes them as they are.
+
+Activations and bias are fp16 or bf16; the output has their type.  Any number of tokens runs in
+the library's kernels (i8_block_linear_forward): up to 128 tokens stream the weight once, more
+take the tensor-core tiles.
+
+Gradients pass straight through the quantisation, in the same 8-bit products
+(i8_block_linear_backward): dx = q(dy) W' with dy in blocks of 128 per token, and for a layer
+that trains its 16-bit weight dW = t(dy)^T t(x) in 128 x 128 tiles, db = sum(dy).
+"""
+from __future__ import annotations
+
+from typing import Iterable, Optional, Tuple
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import abi
+
+DTYPES = (torch.float16, torch.bfloat16)
+
+
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    """Contiguous and on a 16-byte boundary, as the library takes its pointers."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
+def _check_input(x: torch.Tensor, K: int, device: torch.device, name: str = "input"):
+    if x.dtype not in DTYPES:
+        raise TypeError("%s must be fp16 or bf16 (got %s)" % (name, x.dtype))
+    if x.dim() < 1 or x.shape[-1] != K:
+        raise ValueError("last %s dimension %s, expected %d"
+                         % (name, x.shape[-1] if x.dim() else "missing", K))
+    if x.device != device:
+        raise ValueError("%s on %s, layer on %s" % (name, x.device, device))
+
+
+def quantize_weight_blocks(weight: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """e4m3 codes (uint8, the shape of `weight` [..., N, K]) and scales [..., ceil(N/128),
+    ceil(K/128)] of an fp16 or bf16 weight on a CUDA device."""
+    if not weight.is_cuda:
+        raise ValueError("the weight must be on a CUDA device (it is quantised there)")
+    if weight.dtype not in DTYPES:
+        raise TypeError("the weight must be fp16 or bf16 (got %s)" % weight.dtype)
+    w = _dense(weight.detach())
+    N, K = w.shape[-2:]
+    codes = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
+    scales = torch.empty((*w.shape[:-2], (N + 127) // 128, (K + 127) // 128),
+                         dtype=torch.float32, device=w.device)
+    with torch.cuda.device(w.device):
+        abi.i8_block_quantize_weight(w, codes, scales)
+    return codes, scales
+
+
+def _forward(x2, codes, scales, bias):
+    T, K = x2.shape
+    N = codes.shape[0]
+    y = torch.empty((T, N), dtype=x2.dtype, device=x2.device)
+    if T > 0:
+        # the workspace is the caching allocator's: ordered by the stream, and a graph that is
+        # being captured gets one of its own
+        ws = torch.empty((abi.i8_block_linear_workspace_size(T, N, K),), dtype=torch.uint8,
+                         device=x2.device)
+        with torch.cuda.device(x2.device):
+            abi.i8_block_linear_forward(x2, codes, scales, bias, y, ws)
+    return y
+
+
+def _backward(gy, x2, codes, scales, K, want_x, want_w, want_b, dtype):
+    gy = _dense(gy.to(dtype))
+    T, N = gy.shape
+    new = torch.zeros if T == 0 else torch.empty
+    gx = new((T, K), dtype=dtype, device=gy.device) if want_x else None
+    gw = new((N, K), dtype=dtype, device=gy.device) if want_w else None
+    gb = new((N,), dtype=dtype, device=gy.device) if want_b else None
+    if T > 0 and (want_x or want_w or want_b):
+        ws = torch.empty((abi.i8_block_linear_backward_workspace_size(T, N, K),),
+                         dtype=torch.uint8, device=gy.device)
+        with torch.cuda.device(gy.device):
+            abi.i8_block_linear_backward(gy, x2, codes, scales, gx, gw, gb, ws)
+    return gx, gw, gb
+
+
+class _BlockLinearFn(torch.autograd.Function):
+    """Frozen codes: gradients of the input and of the bias."""
+
+    @staticmethod
+    def forward(ctx, x2, codes, scales, bias):
+        ctx.save_for_backward(codes, scales)
+        ctx.dtype = x2.dtype
+        return _forward(x2, codes, scales, bias)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gy):
+        codes, scales = ctx.saved_tensors
+        gx, _, gb = _backward(gy, None, codes, scales, codes.shape[1], ctx.needs_input_grad[0],
+                              False, ctx.needs_input_grad[3], ctx.dtype)
+        return gx, None, None, gb
+
+
+class _BlockLinearTrainFn(torch.autograd.Function):
+    """A 16-bit weight, quantised by every forward: gradients of input, weight and bias."""
+
+    @staticmethod
+    def forward(ctx, x2, weight, bias):
+        codes, scales = quantize_weight_blocks(weight)
+        ctx.save_for_backward(x2, codes, scales)
+        return _forward(x2, codes, scales, bias)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gy):
+        x2, codes, scales = ctx.saved_tensors
+        return _backward(gy, x2, codes, scales, codes.shape[1], *ctx.needs_input_grad, x2.dtype)
+
+
+def linear_block_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                     bias: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y = x W^T + bias with W given as e4m3 codes [N, K] (uint8 or float8_e4m3fn) and scales
+    [ceil(N/128), ceil(K/128)].  x: fp16 or bf16 [..., K], bias: x's type [N]."""
+    if codes.dim() != 2:
+        raise ValueError("codes: a 2-D tensor is required")
+    _check_input(x, codes.shape[1], codes.device)
+    x2 = _dense(x.reshape(-1, codes.shape[1]))
+    if torch.is_grad_enabled() and (x2.requires_grad or (bias is not None and bias.requires_grad)):
+        y = _BlockLinearFn.apply(x2, codes, scales, bias)
+    else:
+        y = _forward(x2, codes, scales, bias)
+    return y.view(*x.shape[:-1], codes.shape[0])
+
+
+def linear_block_fp8_train(x: torch.Tensor, weight: torch.Tensor,
+                           bias: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y = x W^T + bias, the 16-bit weight [N, K] quantised in 128 x 128 tiles by this call;
+    differentiable in x, weight and bias (all of one type, fp16 or bf16)."""
+    if weight.dim() != 2:
+        raise ValueError("weight: a 2-D tensor is required")
+    _check_input(x, weight.shape[1], weight.device)
+    if weight.dtype != x.dtype:
+        raise TypeError("weight is %s, input %s: one type is required" % (weight.dtype, x.dtype))
+    y = _BlockLinearTrainFn.apply(_dense(x.reshape(-1, weight.shape[1])), weight, bias)
+    return y.view(*x.shape[:-1], weight.shape[0])
+
+
+class LinearBlockFp8(torch.nn.Module):
+    """nn.Linear with a block-scaled e4m3 weight.
+
+    Buffers (saved by ``state_dict``): ``CB`` uint8 [out, in] e4m3 codes, ``SCB`` fp32
+    [ceil(out/128), ceil(in/128)], ``bias`` [out] or absent.  With ``has_16bit_weights`` the
+    weight and the bias are parameters of type `dtype` instead, quantised by every forward, and
+    the layer trains; without, it passes the gradient of its input.
+
+    in_features must be a multiple of 16; out_features may be any number.
+    """
+
+    def __init__(self, in_features: int, out_features: int, bias: bool = True, device=None,
+                 dtype: torch.dtype = torch.bfloat16, has_16bit_weights: bool = False):
+        super().__init__()
+        if in_features <= 0 or out_features <= 0 or in_features % 16 != 0:
+            raise ValueError("in_features must be a positive multiple of 16 (row pitch of the "
+                             "codes for TMA); out_features positive")
+        if dtype not in DTYPES:
+            raise TypeError("dtype must be torch.float16 or torch.bfloat16")
+        self.in_features = in_features
+        self.out_features = out_features
+        self.has_16bit_weights = bool(has_16bit_weights)
+        b = torch.zeros((out_features,), dtype=dtype, device=device) if bias else None
+        if self.has_16bit_weights:
+            self.weight = torch.nn.Parameter(
+                torch.zeros((out_features, in_features), dtype=dtype, device=device))
+            self.bias = None if b is None else torch.nn.Parameter(b)
+        else:
+            self.register_buffer("CB", torch.zeros((out_features, in_features),
+                                                   dtype=torch.uint8, device=device))
+            self.register_buffer("SCB", torch.ones(((out_features + 127) // 128,
+                                                    (in_features + 127) // 128),
+                                                   dtype=torch.float32, device=device))
+            self.register_buffer("bias", b)
+
+    @classmethod
+    def from_linear(cls, linear: torch.nn.Linear, has_16bit_weights: bool = False,
+                    dtype: Optional[torch.dtype] = None) -> "LinearBlockFp8":
+        """From an nn.Linear on a CUDA device.  dtype: by default the weight's, if it has 16
+        bits, else bf16 (to which the weight is rounded before it is quantised)."""
+        w = linear.weight
+        if not w.is_cuda:
+            raise ValueError("the weight must be on a CUDA device (it is quantised there)")
+        dtype = dtype or (w.dtype if w.dtype in DTYPES else torch.bfloat16)
+        m = cls(linear.in_features, linear.out_features, bias=linear.bias is not None,
+                device=w.device, dtype=dtype, has_16bit_weights=has_16bit_weights)
+        with torch.no_grad():
+            if has_16bit_weights:
+                m.weight.copy_(w.to(dtype))
+            else:
+                m.CB, m.SCB = quantize_weight_blocks(w.to(dtype))
+            if linear.bias is not None:
+                m.bias.copy_(linear.bias.to(dtype))
+        return m
+
+    @classmethod
+    def from_codes(cls, codes: torch.Tensor, scales: torch.Tensor,
+                   bias: Optional[torch.Tensor] = None,
+                   dtype: torch.dtype = torch.bfloat16) -> "LinearBlockFp8":
+        """From a stored weight: e4m3 codes [N, K] (float8_e4m3fn or uint8) and fp32 scales
+        [ceil(N/128), ceil(K/128)]."""
+        if codes.dim() != 2 or codes.dtype not in (torch.uint8, torch.float8_e4m3fn):
+            raise ValueError("codes: a 2-D tensor of float8_e4m3fn or uint8 is required")
+        N, K = codes.shape
+        if tuple(scales.shape) != ((N + 127) // 128, (K + 127) // 128):
+            raise ValueError("scales of shape %s, expected %s"
+                             % (tuple(scales.shape), ((N + 127) // 128, (K + 127) // 128)))
+        m = cls(K, N, bias=bias is not None, device=codes.device, dtype=dtype)
+        m.CB.copy_(codes.view(torch.uint8))
+        m.SCB.copy_(scales)
+        if bias is not None:
+            m.bias.copy_(bias.to(dtype))
+        return m
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if self.bias is not None and x.dtype != self.bias.dtype:
+            raise TypeError("input must be %s, the bias' type (got %s)" % (self.bias.dtype, x.dtype))
+        if self.has_16bit_weights:
+            return linear_block_fp8_train(x, self.weight, self.bias)
+        return linear_block_fp8(x, self.CB, self.SCB, self.bias)
+
+    def extra_repr(self) -> str:
+        return ("in_features=%d, out_features=%d, bias=%s, has_16bit_weights=%s"
+                % (self.in_features, self.out_features, self.bias is not None,
+                   self.has_16bit_weights))
+
+
+def replace_linear_with_block_fp8(model: torch.nn.Module, skip: Iterable[str] = ("lm_head",),
+                                  has_16bit_weights: bool = False,
+                                  dtype: Optional[torch.dtype] = None) -> torch.nn.Module:
+    """Swap every nn.Linear of `model` (weights on a CUDA device) for a LinearBlockFp8, in
+    place, except modules whose name (last path component) is in `skip`.  Returns `model`."""
+    skip = set(skip)
+    for name, child in list(model.named_children()):
+        if name in skip:
+            continue
+        if isinstance(child, torch.nn.Linear):
+            setattr(model, name, LinearBlockFp8.from_linear(child, has_16bit_weights, dtype))
+        else:
+            replace_linear_with_block_fp8(child, skip, has_16bit_weights, dtype)
+    return model

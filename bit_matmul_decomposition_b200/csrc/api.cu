@@ -10,8 +10,12 @@
 #include <utility>
 
 #include "../../include/i8linear.h"
+#include "block_gemm.cuh"
+#include "block_quant.cuh"
+#include "block_skinny.cuh"
 #include "bwd.cuh"
 #include "common.cuh"
+#include "experts.cuh"
 #include "gemm.cuh"
 #include "gemm_wide.cuh"
 #include "gemv.cuh"
@@ -748,6 +752,8 @@ i8_status forward_impl(const void* X, int64_t T, int64_t K, const int8_t* CB, co
   return I8_OK;
 }
 
+#include "block_api.cuh"
+
 }  // namespace
 
 // ====================================================================== C ABI
@@ -1046,6 +1052,178 @@ i8_status i8_linear_forward_noalloc(const void* X, int64_t T, int64_t K, const i
   if (st != I8_OK) return st;
   return i8_linear_forward(X, T, K, CB, SCB, bias, N, threshold, C, scratch,
                            kStaticScratchBytes, stream);
+}
+
+// ------------------------------------------------------------------ block-scaled e4m3
+i8_status i8_block_quantize_act(const void* X, int32_t dtype, int64_t T, int64_t K, uint8_t* Xq,
+                                float* SX, void* stream) {
+  if (!X || !Xq || !SX || !aligned16(X) || !aligned16(Xq) || !aligned16(SX)) return I8_ERR_INVALID_ARG;
+  if (!dtype16(dtype) || !shape_ok(T, K)) return I8_ERR_INVALID_ARG;
+  DeviceInfo* d;
+  i8_status st = device_info(&d);
+  if (st != I8_OK) return st;
+  blk::QuantArgs q = quant_args(X, T, K);
+  q.Qr = Xq;
+  q.qr_pitch = K;
+  q.Sr = SX;
+  q.rows_out = T;
+  return run_block_quant(dtype, q, 1, false, static_cast<cudaStream_t>(stream));
+}
+
+i8_status i8_block_quantize_weight(const void* W, int32_t dtype, int64_t Z, int64_t N, int64_t K,
+                                   uint8_t* CB, float* SCB, void* stream) {
+  if (!W || !CB || !SCB || !aligned16(W) || !aligned16(CB) || !aligned16(SCB)) return I8_ERR_INVALID_ARG;
+  if (!dtype16(dtype) || !shape_ok(N, K) || !fits_int(Z) || !fits_int(Z * blocks128(N)) ||
+      !fits_int(Z * blocks128(N) * blocks128(K)))
+    return I8_ERR_INVALID_ARG;
+  DeviceInfo* d;
+  i8_status st = device_info(&d);
+  if (st != I8_OK) return st;
+  blk::QuantArgs q = quant_args(W, N, K);
+  q.Qt = CB;
+  q.qt_pitch = K;
+  q.St = SCB;
+  return run_block_quant(dtype, q, Z, false, static_cast<cudaStream_t>(stream));
+}
+
+size_t i8_block_linear_workspace_size(int64_t T, int64_t N, int64_t K) {
+  if (!shape_ok(T, K) || !fits_int(N)) return 0;
+  return linear_ws(T, K).total;
+}
+
+i8_status i8_block_linear_forward(const void* X, int32_t dtype, int64_t T, int64_t K, const uint8_t* CB,
+                                  const float* SCB, const void* bias, int64_t N, void* Y, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  if (!X || !CB || !SCB || !Y || !workspace || !aligned16(X) || !aligned16(CB) || !aligned16(SCB) ||
+      !aligned16(bias) || !aligned16(Y) || !aligned16(workspace))
+    return I8_ERR_INVALID_ARG;
+  if (!dtype16(dtype) || !shape_ok(T, K) || !fits_int(N)) return I8_ERR_INVALID_ARG;
+  if (workspace_bytes < linear_ws(T, K).total) return I8_ERR_INVALID_ARG;
+  DeviceInfo* d;
+  i8_status st = device_info(&d);
+  if (st != I8_OK) return st;
+  return block_linear_forward(X, dtype, T, K, CB, SCB, bias, N, Y, static_cast<uint8_t*>(workspace), *d,
+                              static_cast<cudaStream_t>(stream));
+}
+
+size_t i8_block_linear_backward_workspace_size(int64_t T, int64_t N, int64_t K) {
+  if (!shape_ok(T, K) || !fits_int(N)) return 0;
+  return linear_bwd_ws(T, N, K).total;
+}
+
+i8_status i8_block_linear_backward(const void* dY, const void* X, int32_t dtype, int64_t T, int64_t N, int64_t K,
+                                   const uint8_t* CB, const float* SCB, void* dX, void* dW, void* db,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dY || !workspace || !aligned16(dY) || !aligned16(workspace)) return I8_ERR_INVALID_ARG;
+  if (!dX && !dW && !db) return I8_ERR_INVALID_ARG;
+  if (dX && (!CB || !SCB)) return I8_ERR_INVALID_ARG;
+  if (dW && !X) return I8_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(CB) || !aligned16(SCB) || !aligned16(dX) || !aligned16(dW) || !aligned16(db))
+    return I8_ERR_INVALID_ARG;
+  if (!dtype16(dtype) || !shape_ok(T, K) || !fits_int(N)) return I8_ERR_INVALID_ARG;
+  if (workspace_bytes < linear_bwd_ws(T, N, K).total) return I8_ERR_INVALID_ARG;
+  DeviceInfo* d;
+  i8_status st = device_info(&d);
+  if (st != I8_OK) return st;
+  return block_linear_backward(dY, X, dtype, T, N, K, CB, SCB, dX, dW, db, static_cast<uint8_t*>(workspace), *d,
+                               static_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------------------------ routing and experts
+i8_status i8_route_experts(const void* logits, int32_t dtype, int64_t T, int64_t E, const float* balance,
+                           int32_t score, int64_t n_groups, int64_t top_groups, int64_t k, int32_t renormalize,
+                           float scale, float* weights, int32_t* idx, void* stream) {
+  if (!logits || !weights || !idx || !aligned16(logits) || !aligned16(balance) || !aligned16(weights) || !aligned16(idx))
+    return I8_ERR_INVALID_ARG;
+  if (!route_shape_ok(dtype, T, E, k, score, scale)) return I8_ERR_INVALID_ARG;
+  if (n_groups < 1 || n_groups > moe::MAX_ROUTE_GROUPS || E % n_groups != 0 || top_groups < 1 || top_groups > n_groups)
+    return I8_ERR_INVALID_ARG;
+  DeviceInfo* d;
+  i8_status st = device_info(&d);
+  if (st != I8_OK) return st;
+  moe::RouteArgs a = {};
+  a.logits = logits;
+  a.T = T;
+  a.E = static_cast<int>(E);
+  a.k = static_cast<int>(k);
+  a.groups = static_cast<int>(n_groups);
+  a.top_groups = static_cast<int>(top_groups);
+  a.balance = balance;
+  a.softmax = score == I8_SCORE_SOFTMAX;
+  a.renorm = renormalize != 0;
+  a.scale = scale;
+  a.weights = weights;
+  a.idx = idx;
+  return run_route(a, dtype, false, static_cast<cudaStream_t>(stream));
+}
+
+i8_status i8_route_experts_backward(const void* logits, int32_t dtype, int64_t T, int64_t E, int32_t score, int64_t k,
+                                    int32_t renormalize, float scale, const int32_t* idx, const float* dweights,
+                                    void* dlogits, void* stream) {
+  if (!logits || !dweights || !idx || !dlogits || !aligned16(logits) || !aligned16(dweights) || !aligned16(idx) ||
+      !aligned16(dlogits))
+    return I8_ERR_INVALID_ARG;
+  if (!route_shape_ok(dtype, T, E, k, score, scale)) return I8_ERR_INVALID_ARG;
+  DeviceInfo* d;
+  i8_status st = device_info(&d);
+  if (st != I8_OK) return st;
+  moe::RouteArgs a = {};
+  a.logits = logits;
+  a.T = T;
+  a.E = static_cast<int>(E);
+  a.k = static_cast<int>(k);
+  a.groups = a.top_groups = 1;
+  a.softmax = score == I8_SCORE_SOFTMAX;
+  a.renorm = renormalize != 0;
+  a.scale = scale;
+  a.idx = const_cast<int32_t*>(idx);
+  a.dweights = dweights;
+  a.dlogits = dlogits;
+  return run_route(a, dtype, true, static_cast<cudaStream_t>(stream));
+}
+
+size_t i8_experts_workspace_size(int64_t T, int64_t K, int64_t I, int64_t E, int64_t k) {
+  ExpertsShape x;
+  return experts_shape(T, K, I, E, k, &x) ? experts_ws(x, false).total : 0;
+}
+
+i8_status i8_experts_forward(const void* X, int32_t dtype, int64_t T, int64_t K, const int32_t* idx,
+                             const float* weights, int64_t k, const uint8_t* CB13, const float* S13,
+                             const uint8_t* CB2, const float* S2, int64_t E, int64_t I, void* Y, float* GU,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  const void* need[] = {X, idx, weights, CB13, S13, CB2, S2, Y, workspace};
+  for (const void* p : need)
+    if (!p || !aligned16(p)) return I8_ERR_INVALID_ARG;
+  ExpertsShape x;
+  if (!aligned16(GU) || !dtype16(dtype) || !experts_shape(T, K, I, E, k, &x)) return I8_ERR_INVALID_ARG;
+  if (workspace_bytes < experts_ws(x, false).total) return I8_ERR_INVALID_ARG;
+  DeviceInfo* d;
+  i8_status st = device_info(&d);
+  if (st != I8_OK) return st;
+  return experts_forward(X, dtype, idx, weights, CB13, S13, CB2, S2, x, Y, GU, static_cast<uint8_t*>(workspace), *d,
+                         static_cast<cudaStream_t>(stream));
+}
+
+size_t i8_experts_backward_workspace_size(int64_t T, int64_t K, int64_t I, int64_t E, int64_t k) {
+  ExpertsShape x;
+  return experts_shape(T, K, I, E, k, &x) ? experts_ws(x, true).total : 0;
+}
+
+i8_status i8_experts_backward(const void* dY, int32_t dtype, int64_t T, int64_t K, const int32_t* idx,
+                              const float* weights, int64_t k, const uint8_t* CB13, const float* S13,
+                              const uint8_t* CB2, const float* S2, int64_t E, int64_t I, const float* GU, void* dX,
+                              float* dweights, void* workspace, size_t workspace_bytes, void* stream) {
+  const void* need[] = {dY, idx, weights, CB13, S13, CB2, S2, GU, dX, dweights, workspace};
+  for (const void* p : need)
+    if (!p || !aligned16(p)) return I8_ERR_INVALID_ARG;
+  ExpertsShape x;
+  if (!dtype16(dtype) || !experts_shape(T, K, I, E, k, &x)) return I8_ERR_INVALID_ARG;
+  if (workspace_bytes < experts_ws(x, true).total) return I8_ERR_INVALID_ARG;
+  DeviceInfo* d;
+  i8_status st = device_info(&d);
+  if (st != I8_OK) return st;
+  return experts_backward(dY, dtype, idx, weights, CB13, S13, CB2, S2, x, GU, dX, dweights,
+                          static_cast<uint8_t*>(workspace), *d, static_cast<cudaStream_t>(stream));
 }
 
 

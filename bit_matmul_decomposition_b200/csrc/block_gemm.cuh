@@ -1,0 +1,516 @@
+// block_gemm.cuh -- products of e4m3 codes whose scales change every 128 terms of the sum, on
+// the 5th-generation tensor cores, for batches of many rows:
+//
+//   C[m,n] = sum_b SA[b, m] * SB[b, n/128] * ( sum_{r in block b} A(m,r) * B(n,r) )
+//
+// with b the blocks of 128 along the reduction.  Uses of it (codes q, scales S of
+// block_quant.cuh):
+//   y  = x W^T       A = row codes of x [T,K]       B = tile codes of W [N,K]   both K-major
+//   dx = dy W        A = row codes of dy [T,N]      B = tile codes of W [N,K]   B MN-major
+//   dW = dy^T x      A = tile codes of dy [T,N]     B = tile codes of x [T,K]   both MN-major
+// so a weight is read in its one stored layout in both directions, and nothing is transposed.
+// The rows of A may be split into groups, each with its own B (the experts of a layer).
+//
+// The scales do not commute with the sum, and they are arbitrary fp32 numbers, so the tensor
+// cores' accumulator holds one block (128 terms) at a time: while the MMAs of block b+1 fill
+// one of the two 256-column TMEM accumulators, the eight epilogue warps read block b out of
+// the other (tcgen05.ld) and add it, times its scale, to fp32 sums in registers (128 a thread).
+// A sum of 128 e4m3 products and the fp32 sum over the blocks are the only accumulations.
+//
+// Design (sm_100a): persistent clusters of two CTAs, 256 x 256 output tiles,
+// tcgen05.mma.cta_group::2 kind::f8f6f4 (M = 256, N = 256, K = 32), a ring of six 32 KB stages
+// filled by TMA (no multicast).  Warps: 0 loads A and arms the leader's barrier, 2 loads B,
+// 1 allocates TMEM and (leader lane 0) issues the MMAs, 3 lays out the groups' tiles, 4..11
+// are the epilogue: warp w reads TMEM lanes 32*(w%4).. and columns 128*((w-4)/4)...
+// A thread's row is fixed and its 128 columns share one B scale, so a block costs it 128 FMAs
+// with one scalar factor.  The registers are split 72 / 208 between the first four warps and
+// the epilogue (setmaxnreg): 128 * 72 + 256 * 208 = 62,464 of the 64,512 the CTA starts with.
+//
+// Gated form (kOut = kOutGated, an expert's first product): a tile holds 128 hidden features,
+// each CTA's 128 rows of B being 64 rows of the gate weight and the same 64 of the up weight,
+// so that a thread ends with g and u of the same 64 features of its row.  h = silu(g) * u is
+// formed in fp32, the row's maximum over the 128 features joined between the two threads that
+// hold it, and h leaves as e4m3 row codes and scales: neither g, u nor h goes through memory.
+#pragma once
+
+#include "block_quant.cuh"
+#include "bwd.cuh"
+#include "common.cuh"
+#include "gemm.cuh"
+
+namespace i8 {
+namespace blk {
+
+constexpr int TM = 256, TN = 256, HM = 128, HN = 128;
+constexpr int BK = 128;                       // reduction terms (bytes) per stage = one block
+constexpr int STAGES = 6;
+constexpr int A_BYTES = HM * BK;
+constexpr int STAGE_BYTES = A_BYTES + HN * BK;
+constexpr int THREADS = 384;
+constexpr int EPI_WARP0 = 4;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int GROUP_M = 16;                   // m-tiles per raster group
+constexpr int MAX_GROUPS = 512;
+constexpr int CST_BYTES = 8 * 32 * 64;        // output staging: a 32 x 32 16-bit block a warp
+constexpr int AUX_BYTES = 2 * 2 * 128 * 4;    // bias of the tile's columns, or row maxima
+constexpr int PRE_BYTES = 2064;               // m-tiles before each group
+constexpr int BAR_BYTES = 256;
+constexpr size_t SMEM_BYTES = static_cast<size_t>(STAGES) * STAGE_BYTES + CST_BYTES + AUX_BYTES +
+                              PRE_BYTES + BAR_BYTES + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+static_assert(PRE_BYTES >= (MAX_GROUPS + 1) * 4, "group prefix");
+
+constexpr int REGS_LOW = 72, REGS_EPI = 208;
+constexpr int REGS_NEEDED = (128 * REGS_LOW + 256 * REGS_EPI + THREADS - 1) / THREADS;
+
+enum { kOutF16 = 0, kOutBf16 = 1, kOutF32 = 2, kOutGated = 3 };
+
+struct GemmArgs {
+  int M, Nc;                    // rows of A in all groups; output columns
+  int k_blocks, n_tiles;
+  int groups;                   // 1 with offsets NULL: one group of all M rows
+  const int32_t* offsets;       // [groups + 1] first row of each group
+  int blocks_per_z, z_per_group;   // B's third coordinate: group * z_per_group + block / blocks_per_z
+  const float* SA;              // SA[block * sa_pitch + (row >> sa_shift)]
+  int64_t sa_pitch;
+  int sa_shift;
+  const float* SB;              // SB[group * sb_group + block * sb_block + (col / 128) * sb_col]
+  int64_t sb_group, sb_block, sb_col;
+  const uint16_t* bias;         // [Nc] in the output's type, or NULL
+  void* C;
+  int64_t ldc;
+  bool c_tma;
+  // gated form: codes [M][h_pitch] and scales [ceil(Nc/128)][M] of h; g and u in fp32,
+  // [M][2][Nc], when GU is not NULL.  Nc = hidden features.
+  uint8_t* H;
+  int64_t h_pitch;
+  float* SH;
+  float* GU;
+  uint64_t wait_limit_ns;
+};
+
+struct SmemBars {
+  uint64_t full[STAGES];
+  uint64_t empty[STAGES];
+  uint64_t tmem_full[2];
+  uint64_t tmem_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(SmemBars) <= BAR_BYTES, "barrier block");
+
+__device__ __forceinline__ void epi_bar256() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// every bulk store of this thread has read its shared-memory source
+__device__ __forceinline__ void bulk_wait_read_0() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
+// sigmoid(g) for silu(g) = g * sigmoid(g).  exp(-g) = 2^hi * 2^lo with hi + lo = -g * log2(e) to about 2^-47 relative, so
+// the result is within a few units in the last place of fp32.  For g below about -88, exp(-g)
+// overflows to infinity and g / inf = -0: the limit.  g = -inf would be 0 * inf and gives NaN.
+__device__ __forceinline__ float fast_sigmoid(float g) {
+  const float c1 = 1.4426950216293335f, c2 = 1.9259629911266175e-8f;   // log2(e) = c1 + c2
+  const float hi = -g * c1;
+  const float lo = fmaf(-g, c1, -hi) - g * c2;
+  float e;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(hi));
+  e = fmaf(e, lo * 0.6931471805599453f, e);
+  // hi beyond the exponent range: e is inf (or 0); lo may then be NaN or tiny, so pin the limits
+  e = hi > 128.0f ? __int_as_float(0x7f800000) : e;
+  return __fdividef(1.0f, 1.0f + e);
+}
+
+// position of tile t of a group of m_tiles x n_tiles: GROUP_M m-tiles, then the next n-tile
+__device__ __forceinline__ void raster(int t, int m_tiles, int n_tiles, int& mt, int& nt) {
+  const int G = m_tiles < GROUP_M ? m_tiles : GROUP_M;
+  const int group = t / (G * n_tiles);
+  const int r = t - group * (G * n_tiles);
+  const int mb = group * G;
+  const int rows = (m_tiles - mb) < G ? (m_tiles - mb) : G;
+  mt = mb + r % rows;
+  nt = r / rows;
+}
+
+template <bool kAMN, bool kBMN, int kOut>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    block_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
+                      const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmC, const GemmArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_s = smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw_s & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t ring = raw_s + pad;
+  const uint32_t cstage = ring + static_cast<uint32_t>(STAGES * STAGE_BYTES);
+  float* aux = reinterpret_cast<float*>(smem + static_cast<size_t>(STAGES) * STAGE_BYTES + CST_BYTES);
+  int* pre = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(aux) + AUX_BYTES);
+  SmemBars* bars = reinterpret_cast<SmemBars*>(reinterpret_cast<uint8_t*>(pre) + PRE_BYTES);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = gemm::cluster_rank();
+  volatile int* abort_flag = &bars->abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&bars->full[s]), 1);
+      mbar_init(smem_u32(&bars->empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&bars->tmem_full[b]), 1);
+      mbar_init(smem_u32(&bars->tmem_empty[b]), 16);   // 8 epilogue warps x 2 CTAs
+    }
+    mbar_init(smem_u32(&bars->drain), 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    if (a.c_tma) tma_prefetch_desc(&tmC);
+  }
+  if (warp == 1) {
+    gemm::tmem_alloc_pair(smem_u32(&bars->tmem_base), TMEM_COLS);
+    gemm::tmem_relinquish_pair();
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  if (warp == 3) {
+    // m-tiles before each group: every lane sums its run of groups, then a scan over lanes
+    if (a.offsets == nullptr) {
+      if (lane == 0) {
+        pre[0] = 0;
+        pre[1] = (a.M + TM - 1) / TM;
+      }
+    } else {
+      const int per = (a.groups + 31) / 32;
+      const int g0 = min(lane * per, a.groups), g1 = min(g0 + per, a.groups);
+      int sum = 0;
+      for (int g = g0; g < g1; ++g) sum += (__ldg(a.offsets + g + 1) - __ldg(a.offsets + g) + TM - 1) / TM;
+      int run = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += x;
+      }
+      if (lane == 31) pre[a.groups] = run;
+      run -= sum;
+      for (int g = g0; g < g1; ++g) {
+        pre[g] = run;
+        run += (__ldg(a.offsets + g + 1) - __ldg(a.offsets + g) + TM - 1) / TM;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  gemm::cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = bars->tmem_base;
+
+  const int KB = a.k_blocks;
+  const int num_tiles = pre[a.groups] * a.n_tiles;
+  const int cluster_id = blockIdx.x >> 1;
+  const int num_clusters = gridDim.x >> 1;
+  const uint64_t lim = a.wait_limit_ns;
+  // tile t: its group, first row, the end of the group's rows, and its n-tile
+  auto tile_at = [&](int t, int& g, int& row0, int& row_end, int& nt) {
+    int lo = 0, hi = a.groups - 1;                // the last group whose first tile is <= t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] * a.n_tiles <= t) lo = mid; else hi = mid - 1;
+    }
+    g = lo;
+    const int m_tiles = pre[g + 1] - pre[g];
+    int mt;
+    raster(t - pre[g] * a.n_tiles, m_tiles, a.n_tiles, mt, nt);
+    row0 = mt * TM;
+    row_end = a.M;
+    if (a.offsets != nullptr) {
+      row0 += __ldg(a.offsets + g);
+      row_end = __ldg(a.offsets + g + 1);
+    }
+  };
+
+  if (warp < EPI_WARP0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_LOW));
+    if (warp == 0 || warp == 2) {
+      if (lane == 0) {
+        // -------------------------------------------------------------- TMA producers
+        const bool loads_a = (warp == 0);
+        const uint32_t full_leader0 = gemm::map_to_rank(smem_u32(&bars->full[0]), 0);
+        int s = 0;
+        uint32_t ph = 0, issued = 0;
+        bool ok = true;
+        for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
+          int g, row0, row_end, nt;
+          tile_at(t, g, row0, row_end, nt);
+          const int m0 = row0 + static_cast<int>(rank) * HM;
+          const int n0 = nt * TN + static_cast<int>(rank) * HN;
+          const int z0 = g * a.z_per_group;
+          int zb = 0, kz = 0;                       // block / blocks_per_z, block % blocks_per_z
+          for (int kb = 0; kb < KB; ++kb) {
+            if (!mbar_wait(smem_u32(&bars->empty[s]), ph ^ 1u, abort_flag, lim)) {
+              ok = false;
+              break;
+            }
+            const uint32_t dst = ring + s * STAGE_BYTES + (loads_a ? 0u : static_cast<uint32_t>(A_BYTES));
+            if (loads_a && rank == 0)
+              mbar_arrive_expect_tx(smem_u32(&bars->full[s]), 2 * STAGE_BYTES);
+            const uint32_t fb = full_leader0 + static_cast<uint32_t>(s) * 8u;
+            if (loads_a) {
+              if (kAMN)
+                gemm::tma_load_2d_pair(dst, &tmA, fb, m0, kb * BK);
+              else
+                gemm::tma_load_2d_pair(dst, &tmA, fb, kb * BK, m0);
+            } else if (kOut == kOutGated) {
+              const int i0 = nt * HN + static_cast<int>(rank) * 64;
+              gemm::tma_load_3d_pair(dst, &tmB, fb, kb * BK, i0, z0);
+              gemm::tma_load_3d_pair(dst + 8192u, &tmB, fb, kb * BK, i0, z0 + 1);
+            } else if (kBMN) {
+              gemm::tma_load_3d_pair(dst, &tmB, fb, n0, kz * BK, z0 + zb);
+              if (++kz == a.blocks_per_z) {
+                kz = 0;
+                ++zb;
+              }
+            } else {
+              gemm::tma_load_3d_pair(dst, &tmB, fb, kb * BK, n0, z0);
+            }
+            ++issued;
+            if (++s == STAGES) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+        if (!ok && loads_a && rank == 0) {
+          // wind down: wait (bounded, ignoring the abort flag) for the copies in flight
+          int no_abort = 0;
+          const uint32_t inflight = issued < STAGES ? issued : STAGES;
+          for (uint32_t i = 0; i < inflight; ++i) {
+            const uint32_t u = issued - 1 - i;
+            mbar_wait(smem_u32(&bars->full[u % STAGES]), (u / STAGES) & 1u, &no_abort, lim);
+          }
+        }
+      }
+    } else if (warp == 1) {
+      if (lane == 0 && rank == 0) {
+        // -------------------------------------------------------------- MMA issuer
+        constexpr uint32_t ID = idesc_e4m3_f32(TM, TN) | (kAMN ? (1u << 15) : 0u) | (kBMN ? (1u << 16) : 0u);
+        int s = 0;
+        uint32_t ph = 0, n = 0;                     // n: blocks issued so far
+        bool ok = true;
+        for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
+          for (int kb = 0; kb < KB; ++kb, ++n) {
+            const uint32_t b = n & 1u;
+            if (!mbar_wait(smem_u32(&bars->tmem_empty[b]), ((n >> 1) & 1u) ^ 1u, abort_flag, lim) ||
+                !mbar_wait(smem_u32(&bars->full[s]), ph, abort_flag, lim)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = ring + s * STAGE_BYTES;
+            const uint32_t sb = sa + A_BYTES;
+            const uint32_t d = tmem_base + b * TN;
+#pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk) {
+              // 32 terms further: 32 bytes along a K-major row, 32 rows of 128 bytes otherwise
+              const uint64_t ad = kAMN ? bwd::sdesc_mn_sw128(sa + kk * 4096) : sdesc_k_sw128(sa + kk * 32);
+              const uint64_t bd = kBMN ? bwd::sdesc_mn_sw128(sb + kk * 4096) : sdesc_k_sw128(sb + kk * 32);
+              gemm::umma_e4m3_pair(d, ad, bd, ID, kk != 0);
+            }
+            gemm::umma_commit_pair(smem_u32(&bars->empty[s]));
+            gemm::umma_commit_pair(smem_u32(&bars->tmem_full[b]));
+            if (++s == STAGES) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+        int no_abort = 0;
+        gemm::umma_commit_pair(smem_u32(&bars->drain));
+        mbar_wait(smem_u32(&bars->drain), 0u, &no_abort, lim);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
+    // ------------------------------------------------------------------ epilogue
+    const int q = warp & 3;
+    const int half = (warp - EPI_WARP0) >> 2;       // which 128 columns
+    const int et = threadIdx.x - EPI_WARP0 * 32;    // 0..255
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * HN);
+    const uint32_t cst = cstage + static_cast<uint32_t>((warp - EPI_WARP0) * 2048);
+    const uint32_t empty_leader0 = gemm::map_to_rank(smem_u32(&bars->tmem_empty[0]), 0);
+    uint32_t n = 0;
+    int parity = 0;
+    // after a wait that ran out, a warp keeps walking the tiles (it must meet the others at
+    // the named barrier) but touches TMEM and memory no more
+    bool dead = false;
+    for (int t = cluster_id; t < num_tiles; t += num_clusters, parity ^= 1) {
+      int g, row0, row_end, nt;
+      tile_at(t, g, row0, row_end, nt);
+      const int wrow0 = row0 + static_cast<int>(rank) * HM + q * 32;   // the warp's first row
+      const int row = wrow0 + lane;
+      const bool row_ok = row < row_end;
+      const int n0 = nt * TN + half * HN;
+      if (kOut != kOutGated) {
+        const int c = nt * TN + et;
+        float bv = 0.0f;
+        if (a.bias != nullptr && c < a.Nc)
+          bv = kOut == kOutBf16 ? load16<true>(a.bias + c) : load16<false>(a.bias + c);
+        aux[parity * 256 + et] = bv;
+        epi_bar256();
+      }
+      const float* sa = a.SA + ((row < a.M ? row : a.M - 1) >> a.sa_shift);
+      const float* sb0;
+      const float* sb1 = nullptr;
+      if (kOut == kOutGated) {
+        sb0 = a.SB + g * a.sb_group + nt * a.sb_col;
+        sb1 = sb0 + (a.sb_group >> 1);
+      } else {
+        const int cb = n0 < a.Nc ? n0 >> 7 : 0;     // a half past the last column: any scale
+        sb0 = a.SB + g * a.sb_group + cb * a.sb_col;
+      }
+      float acc[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+      float s0 = 0.0f, s1 = 0.0f;
+      if (!dead) {
+        const float v = __ldg(sa);
+        s0 = v * __ldg(sb0);
+        if (kOut == kOutGated) s1 = v * __ldg(sb1);
+      }
+      for (int kb = 0; kb < KB && !dead; ++kb, ++n) {
+        const uint32_t b = n & 1u;
+        float s0n = 0.0f, s1n = 0.0f;               // the next block's scales, ahead of the wait
+        if (kb + 1 < KB) {
+          const float v = __ldg(sa + static_cast<int64_t>(kb + 1) * a.sa_pitch);
+          s0n = v * __ldg(sb0 + static_cast<int64_t>(kb + 1) * a.sb_block);
+          if (kOut == kOutGated) s1n = v * __ldg(sb1 + static_cast<int64_t>(kb + 1) * a.sb_block);
+        }
+        const bool got = mbar_wait(smem_u32(&bars->tmem_full[b]), (n >> 1) & 1u, abort_flag, lim);
+        if (!__all_sync(0xffffffffu, got)) {
+          dead = true;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t tb = lane_base + b * TN;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(tb + static_cast<uint32_t>(c * 32), r);
+          tmem_ld_wait_regs(r);
+          const float s = (kOut == kOutGated && c >= 2) ? s1 : s0;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc[c * 32 + j] = fmaf(__uint_as_float(r[j]), s, acc[c * 32 + j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) gemm::mbar_arrive_remote(empty_leader0 + b * 8u);
+        s0 = s0n;
+        s1 = s1n;
+      }
+      if (kOut == kOutGated) {
+        // acc[0..63] = g, acc[64..127] = u of features i0 .. i0 + 63
+        const int i0 = nt * HN + half * 64;
+        float am = 0.0f;
+        if (a.GU != nullptr && row_ok && !dead) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            float* dst = a.GU + (static_cast<int64_t>(row) * 2 + w) * a.Nc + i0;
+#pragma unroll
+            for (int j = 0; j < 64; j += 4)          // Nc % 16 == 0: four features stay together
+              if (i0 + j < a.Nc)
+                *reinterpret_cast<float4*>(dst + j) = make_float4(acc[w * 64 + j], acc[w * 64 + j + 1], acc[w * 64 + j + 2], acc[w * 64 + j + 3]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 64; ++j) {
+          const float gv = acc[j];
+          acc[j] = gv * fast_sigmoid(gv) * acc[64 + j];
+          am = fmaxf(am, fabsf(acc[j]));
+        }
+        float* mx = aux + parity * 256;              // [half][128 rows of this CTA]
+        mx[half * 128 + q * 32 + lane] = am;
+        epi_bar256();
+        am = fmaxf(fmaxf(am, mx[(half ^ 1) * 128 + q * 32 + lane]), kScaleFloor);
+        if (row_ok && !dead) {
+          const float up = block_up(am);
+          uint4* dst = reinterpret_cast<uint4*>(a.H + static_cast<int64_t>(row) * a.h_pitch + i0);
+#pragma unroll
+          for (int j = 0; j < 64; j += 16) {
+            const float f0[8] = {acc[j], acc[j + 1], acc[j + 2], acc[j + 3], acc[j + 4], acc[j + 5], acc[j + 6], acc[j + 7]};
+            const float f1[8] = {acc[j + 8], acc[j + 9], acc[j + 10], acc[j + 11], acc[j + 12], acc[j + 13], acc[j + 14], acc[j + 15]};
+            const uint2 x = codes8_scaled(f0, up), y = codes8_scaled(f1, up);
+            dst[j >> 4] = make_uint4(x.x, x.y, y.x, y.y);
+          }
+          if (half == 0) a.SH[static_cast<int64_t>(nt) * a.M + row] = block_down(am);
+        }
+      } else if (!dead && n0 < a.Nc && wrow0 < row_end) {
+        const float* bs = aux + parity * 256 + half * HN;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int c0 = n0 + c * 32;
+          if (c0 >= a.Nc) continue;
+          if (kOut == kOutF32) {
+            if (row_ok) {
+              float* dst = static_cast<float*>(a.C) + static_cast<int64_t>(row) * a.ldc + c0;
+              if ((a.ldc & 3) == 0 && c0 + 32 <= a.Nc) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4)
+                  *reinterpret_cast<float4*>(dst + j) = make_float4(acc[c * 32 + j], acc[c * 32 + j + 1], acc[c * 32 + j + 2], acc[c * 32 + j + 3]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (c0 + j < a.Nc) dst[j] = acc[c * 32 + j];
+              }
+            }
+            continue;
+          }
+          uint32_t o[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            o[j] = pack2<kOut == kOutBf16>(acc[c * 32 + 2 * j] + bs[c * 32 + 2 * j], acc[c * 32 + 2 * j + 1] + bs[c * 32 + 2 * j + 1]);
+          if (a.c_tma) {
+            // 32 rows x 32 columns through shared memory, one TMA store, clipped by the map
+            if (lane == 0) bulk_wait_read_0();
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              gemm::sts_v4(cst + static_cast<uint32_t>(lane * 64 + j * 16), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            gemm::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              gemm::tma_store_2d(&tmC, cst, c0, wrow0);
+              gemm::bulk_commit();
+            }
+          } else if (row_ok) {
+            uint16_t* dst = static_cast<uint16_t*>(a.C) + static_cast<int64_t>(row) * a.ldc + c0;
+            if ((a.ldc & 7) == 0 && c0 + 32 <= a.Nc) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                reinterpret_cast<uint4*>(dst)[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (c0 + j < a.Nc) dst[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+            }
+          }
+        }
+      }
+    }
+    if (lane == 0) gemm::bulk_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  gemm::cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    gemm::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+  gemm::cluster_sync();
+}
+
+}  // namespace blk
+}  // namespace i8

@@ -1,0 +1,423 @@
+// block_skinny.cuh -- the forward product of block_gemm.cuh for batches of few rows (a decode
+// batch, or the few tokens of each expert), where streaming the weight is all the time:
+//
+//   C[t,n] = sum_b SA[b, t] * SB[b, n/128] * ( sum_{r in block b} A(t,r) * B(n,r) )
+//
+// The roles of the operands are swapped: 128 rows of the weight are the tensor cores' M, and
+// NT = 16..128 tokens their N, so that one token costs an MMA of N = 16 and not of M = 128.
+// TMEM lanes are then output features and columns tokens; the weight's scale is one number for
+// a whole tile and block, the tokens' scales differ by column and come through shared memory.
+//
+// The bound is HBM: each weight byte is read once.  To keep all SMs reading to the end, the
+// (tile, block) units of the whole product are dealt out in equal contiguous runs, one run a
+// CTA, whatever tile they fall in.  A tile that one CTA ran alone is written at once; the
+// others leave fp32 partial sums in the workspace, and the CTA that arrives last (a counter)
+// adds the parts of the tile in the order of the CTAs and writes it: the order of arrival
+// changes nothing in the result, and no CTA waits for another.
+//
+// Design (sm_100a): one CTA an SM; warp 0 fills a ring of [128 x 128 weight | NT x 128 token]
+// stages by TMA, warp 1 issues tcgen05.mma (cta_group::1, kind::f8f6f4, M = 128, N = NT), one
+// block to one of NBUF small TMEM accumulators, warps 2..5 add them, scaled, to fp32 sums in
+// registers.  The weight does not depend on the kernel before (the quantiser of the tokens), so
+// with a tile order known from the start the ring fills with weights while that kernel runs.
+#pragma once
+
+#include "block_gemm.cuh"
+
+namespace i8 {
+namespace skinny {
+
+using blk::BK;
+using blk::MAX_GROUPS;
+constexpr int ROWS = 128;                    // weight rows of a tile
+constexpr int W_BYTES = ROWS * BK;
+constexpr int THREADS = 192;
+constexpr int PRE_BYTES = blk::PRE_BYTES;
+constexpr int BAR_BYTES = 512;
+constexpr int MAX_STAGES = 12;
+constexpr int NBUF = 4;                      // TMEM accumulators
+constexpr int RING_BUDGET = 212 * 1024;
+
+__host__ __device__ constexpr int stage_bytes(int nt) { return W_BYTES + nt * BK; }
+__host__ __device__ constexpr int stages(int nt) {
+  return RING_BUDGET / stage_bytes(nt) < MAX_STAGES ? RING_BUDGET / stage_bytes(nt) : MAX_STAGES;
+}
+__host__ __device__ constexpr int scale_bytes(int nt) { return 4 * 2 * nt * 4; }
+__host__ __device__ constexpr size_t smem_bytes(int nt) {
+  return static_cast<size_t>(stages(nt)) * stage_bytes(nt) + scale_bytes(nt) + PRE_BYTES + BAR_BYTES + 1024;
+}
+static_assert(smem_bytes(16) <= 232448 && smem_bytes(32) <= 232448 && smem_bytes(64) <= 232448 &&
+              smem_bytes(128) <= 232448, "shared memory per CTA");
+
+struct Args {
+  int M;                        // rows (tokens) in all groups
+  int k_blocks;
+  int n_tiles, n_per_z;         // weight tiles of a group; of one z slice of it
+  int z_cols;                   // output columns of one z slice
+  int groups;
+  const int32_t* offsets;       // as in GemmArgs
+  int z_per_group;
+  const float* SA;              // [k_blocks][M]
+  const float* SB;              // [z][n_per_z][k_blocks]
+  const uint16_t* bias;         // [z_cols] in the output's type, or NULL (one z slice)
+  void* C;                      // [M][ldc]
+  int64_t ldc;
+  float* parts;                 // [2 * grid][NT][128]
+  unsigned int* arrived;        // [grid], zero at the start
+  uint64_t wait_limit_ns;
+};
+
+struct SmemBars {
+  uint64_t full[MAX_STAGES];
+  uint64_t empty[MAX_STAGES];
+  uint64_t tmem_full[NBUF];
+  uint64_t tmem_empty[NBUF];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  unsigned int last;
+};
+static_assert(sizeof(SmemBars) <= BAR_BYTES, "barrier block");
+
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 lanes x 16 consecutive 32-bit columns of TMEM into 16 registers, and the wait for them.
+__device__ __forceinline__ void tmem_ld_x16_wait(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void epi_bar128() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+template <int NT, int kOut>
+__global__ void __launch_bounds__(THREADS, 1)
+    block_skinny_kernel(const __grid_constant__ CUtensorMap tmW,
+                        const __grid_constant__ CUtensorMap tmX, const Args a) {
+  constexpr int STAGES = stages(NT);
+  constexpr int SBYTES = stage_bytes(NT);
+  constexpr uint32_t TMEM_COLS = NBUF * NT < 32 ? 32 : NBUF * NT;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_s = smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw_s & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t ring = raw_s + pad;
+  float* sscale = reinterpret_cast<float*>(smem + static_cast<size_t>(STAGES) * SBYTES);
+  int* pre = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(sscale) + scale_bytes(NT));
+  SmemBars* bars = reinterpret_cast<SmemBars*>(reinterpret_cast<uint8_t*>(pre) + PRE_BYTES);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  volatile int* abort_flag = &bars->abort_flag;
+  const uint64_t lim = a.wait_limit_ns;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&bars->full[s]), 1);
+      mbar_init(smem_u32(&bars->empty[s]), 1);
+    }
+    for (int b = 0; b < NBUF; ++b) {
+      mbar_init(smem_u32(&bars->tmem_full[b]), 1);
+      mbar_init(smem_u32(&bars->tmem_empty[b]), 4);
+    }
+    mbar_init(smem_u32(&bars->drain), 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&bars->tmem_base), TMEM_COLS);
+    tmem_relinquish();
+  }
+  const bool grouped = a.offsets != nullptr;
+  if (grouped) {
+    grid_dep_wait();
+    grid_dep_launch();
+  }
+  if (warp == 2) {
+    // token tiles before each group
+    if (!grouped) {
+      if (lane == 0) {
+        pre[0] = 0;
+        pre[1] = (a.M + NT - 1) / NT;
+      }
+    } else {
+      const int per = (a.groups + 31) / 32;
+      const int g0 = min(lane * per, a.groups), g1 = min(g0 + per, a.groups);
+      int sum = 0;
+      for (int g = g0; g < g1; ++g) sum += (__ldg(a.offsets + g + 1) - __ldg(a.offsets + g) + NT - 1) / NT;
+      int run = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += x;
+      }
+      if (lane == 31) pre[a.groups] = run;
+      run -= sum;
+      for (int g = g0; g < g1; ++g) {
+        pre[g] = run;
+        run += (__ldg(a.offsets + g + 1) - __ldg(a.offsets + g) + NT - 1) / NT;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = bars->tmem_base;
+
+  const int KB = a.k_blocks;
+  const int64_t units = static_cast<int64_t>(pre[a.groups]) * a.n_tiles * KB;
+  // G CTAs share the units, each at least one: with fewer units than CTAs (known only here, by
+  // the groups' sizes) the CTAs past the last unit have none and take no part in any tile
+  const int64_t G = units < static_cast<int64_t>(gridDim.x) ? units : static_cast<int64_t>(gridDim.x);
+  auto first_unit = [&](int64_t c) -> int64_t { return units * c / G; };
+  const bool idle = static_cast<int64_t>(blockIdx.x) >= G;
+  const int64_t u0 = idle ? 0 : first_unit(blockIdx.x);
+  const int64_t u1 = idle ? 0 : first_unit(static_cast<int64_t>(blockIdx.x) + 1);
+  // tile: its group, first token, end of the group's tokens, z slice and weight tile in it
+  auto tile_at = [&](int tile, int& row0, int& row_end, int& z, int& nz) {
+    int lo = 0, hi = a.groups - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] * a.n_tiles <= tile) lo = mid; else hi = mid - 1;
+    }
+    const int tt = pre[lo + 1] - pre[lo];
+    const int r = tile - pre[lo] * a.n_tiles;
+    const int nt = r / tt;                        // the token tiles of one weight tile in turn
+    row0 = (r - nt * tt) * NT;
+    row_end = a.M;
+    if (grouped) {
+      row0 += __ldg(a.offsets + lo);
+      row_end = __ldg(a.offsets + lo + 1);
+    }
+    const int zz = nt / a.n_per_z;
+    z = lo * a.z_per_group + zz;
+    nz = nt - zz * a.n_per_z;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------------------------------------------------------- TMA producer
+      // One pass over the run.  While the kernel before may still write the tokens' codes
+      // (dense form), the first STAGES units get their weight half only; then the wait, their
+      // token halves, and the rest of the run whole.
+      const int64_t head = grouped ? 0 : (u1 - u0 < STAGES ? u1 - u0 : STAGES);
+      auto issue = [&](int64_t u, int s, bool w, bool x, int& row0, int& z, int& nz, int& last_tile) {
+        const int tile = static_cast<int>(u / KB);
+        const int kb = static_cast<int>(u - static_cast<int64_t>(tile) * KB);
+        if (tile != last_tile) {
+          int row_end;
+          tile_at(tile, row0, row_end, z, nz);
+          last_tile = tile;
+        }
+        const uint32_t dst = ring + s * SBYTES;
+        const uint32_t fb = smem_u32(&bars->full[s]);
+        if (w) {
+          mbar_arrive_expect_tx(fb, SBYTES);
+          tma_load_3d(dst, &tmW, fb, kb * BK, nz * ROWS, z);
+        }
+        if (x) tma_load_2d(dst + W_BYTES, &tmX, fb, kb * BK, row0);
+      };
+      int row0 = 0, z = 0, nz = 0, last_tile = -1;
+      for (int64_t i = 0; i < head; ++i) issue(u0 + i, static_cast<int>(i), true, false, row0, z, nz, last_tile);
+      if (!grouped) {
+        grid_dep_wait();
+        grid_dep_launch();
+      }
+      last_tile = -1;
+      for (int64_t i = 0; i < head; ++i) issue(u0 + i, static_cast<int>(i), false, true, row0, z, nz, last_tile);
+      int s = static_cast<int>(head % STAGES);
+      uint32_t ph = head == STAGES ? 1u : 0u;
+      uint32_t issued = static_cast<uint32_t>(head);
+      bool ok = true;
+      for (int64_t u = u0 + head; u < u1; ++u) {
+        if (!mbar_wait(smem_u32(&bars->empty[s]), ph ^ 1u, abort_flag, lim)) {
+          ok = false;
+          break;
+        }
+        issue(u, s, true, true, row0, z, nz, last_tile);
+        ++issued;
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      if (!ok) {
+        int no_abort = 0;
+        const uint32_t inflight = issued < STAGES ? issued : STAGES;
+        for (uint32_t i = 0; i < inflight; ++i) {
+          const uint32_t u = issued - 1 - i;
+          mbar_wait(smem_u32(&bars->full[u % STAGES]), (u / STAGES) & 1u, &no_abort, lim);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---------------------------------------------------------------- MMA issuer
+      constexpr uint32_t ID = idesc_e4m3_f32(ROWS, NT);
+      int s = 0;
+      uint32_t ph = 0, n = 0;
+      for (int64_t u = u0; u < u1; ++u, ++n) {
+        const uint32_t b = n % NBUF;
+        if (!mbar_wait(smem_u32(&bars->tmem_empty[b]), ((n / NBUF) & 1u) ^ 1u, abort_flag, lim) ||
+            !mbar_wait(smem_u32(&bars->full[s]), ph, abort_flag, lim))
+          break;
+        tc_fence_after();
+        const uint32_t sw = ring + s * SBYTES;
+#pragma unroll
+        for (int kk = 0; kk < BK / 32; ++kk)
+          umma_e4m3(tmem_base + b * NT, sdesc_k_sw128(sw + kk * 32), sdesc_k_sw128(sw + W_BYTES + kk * 32), ID, kk != 0);
+        umma_commit(smem_u32(&bars->empty[s]));
+        umma_commit(smem_u32(&bars->tmem_full[b]));
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      int no_abort = 0;
+      umma_commit(smem_u32(&bars->drain));
+      mbar_wait(smem_u32(&bars->drain), 0u, &no_abort, lim);
+    }
+  } else {
+    // ------------------------------------------------------------------ epilogue
+    if (!grouped) grid_dep_wait();
+    const int q = warp & 3;
+    const int nl = q * 32 + lane;                   // the thread's weight row in the tile
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    float* sc = sscale + q * 2 * NT;                // this warp's two rows of scales
+    constexpr int SL = (NT + 31) / 32;              // scales a lane loads
+    uint32_t n = 0;
+    bool dead = false;
+    for (int64_t u = u0; u < u1;) {
+      const int tile = static_cast<int>(u / KB);
+      const int64_t t0 = static_cast<int64_t>(tile) * KB;
+      const int kb0 = static_cast<int>(u - t0);
+      const int kb1 = static_cast<int>((t0 + KB < u1 ? t0 + KB : u1) - t0);
+      int row0, row_end, z, nz;
+      tile_at(tile, row0, row_end, z, nz);
+      const float* sb = a.SB + (static_cast<int64_t>(z) * a.n_per_z + nz) * KB;
+      float acc[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[j] = 0.0f;
+      float nx[SL];
+      auto load_scales = [&](int kb) {
+        const float w = __ldg(sb + kb);
+#pragma unroll
+        for (int i = 0; i < SL; ++i) {
+          const int t = row0 + lane + 32 * i;
+          nx[i] = __ldg(a.SA + static_cast<int64_t>(kb) * a.M + (t < a.M ? t : a.M - 1)) * w;
+        }
+      };
+      if (!dead) load_scales(kb0);
+      for (int kb = kb0; kb < kb1 && !dead; ++kb, ++n) {
+        const uint32_t b = n % NBUF;
+        float* row = sc + (n & 1u) * NT;
+#pragma unroll
+        for (int i = 0; i < SL; ++i)
+          if (lane + 32 * i < NT) row[lane + 32 * i] = nx[i];
+        __syncwarp();
+        if (kb + 1 < kb1) load_scales(kb + 1);
+        const bool got = mbar_wait(smem_u32(&bars->tmem_full[b]), (n / NBUF) & 1u, abort_flag, lim);
+        if (!__all_sync(0xffffffffu, got)) {
+          dead = true;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < NT / 16; ++c) {
+          uint32_t r[16];
+          tmem_ld_x16_wait(lane_base + b * NT + c * 16, r);
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 s4 = *reinterpret_cast<const float4*>(row + c * 16 + j);
+            acc[c * 16 + j] = fmaf(__uint_as_float(r[j]), s4.x, acc[c * 16 + j]);
+            acc[c * 16 + j + 1] = fmaf(__uint_as_float(r[j + 1]), s4.y, acc[c * 16 + j + 1]);
+            acc[c * 16 + j + 2] = fmaf(__uint_as_float(r[j + 2]), s4.z, acc[c * 16 + j + 2]);
+            acc[c * 16 + j + 3] = fmaf(__uint_as_float(r[j + 3]), s4.w, acc[c * 16 + j + 3]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->tmem_empty[b]));
+      }
+      u = t0 + kb1;
+      bool write = !dead;
+      if (kb0 != 0 || kb1 != KB) {
+        // the CTAs that share this tile, and this one's part of it
+        const int64_t me = blockIdx.x;
+        int64_t c0 = t0 * G / units, c1 = (t0 + KB - 1) * G / units;   // estimates, then exact
+        while (c0 > 0 && first_unit(c0) > t0) --c0;
+        while (first_unit(c0 + 1) <= t0) ++c0;
+        while (c1 > 0 && first_unit(c1) > t0 + KB - 1) --c1;
+        while (first_unit(c1 + 1) <= t0 + KB - 1) ++c1;
+        auto slot = [&](int64_t c) { return 2 * c + (first_unit(c) / KB == tile ? 0 : 1); };
+        float* part = a.parts + slot(me) * (NT * ROWS) + nl;
+        if (!dead) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j) part[j * ROWS] = acc[j];
+        }
+        __threadfence();
+        epi_bar128();
+        if (threadIdx.x == 64) bars->last = dead ? 0u : atomicAdd(a.arrived + c0, 1u);
+        epi_bar128();
+        write = !dead && bars->last == static_cast<unsigned int>(c1 - c0);
+        epi_bar128();                               // `last` is free for the next tile
+        if (write) {
+          __threadfence();
+#pragma unroll
+          for (int j = 0; j < NT; ++j) acc[j] = 0.0f;
+          for (int64_t c = c0; c <= c1; ++c) {
+            const float* p = a.parts + slot(c) * (NT * ROWS) + nl;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[j] += __ldcg(p + j * ROWS);
+          }
+        }
+      }
+      const int col_z = nz * ROWS + nl;
+      if (write && col_z < a.z_cols) {
+        const int zz = z % a.z_per_group;
+        const int64_t col = static_cast<int64_t>(zz) * a.z_cols + col_z;
+        float bv = 0.0f;
+        if (a.bias != nullptr)
+          bv = kOut == blk::kOutBf16 ? blk::load16<true>(a.bias + col) : blk::load16<false>(a.bias + col);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int64_t t = row0 + j;
+          if (t < row_end) {
+            if (kOut == blk::kOutF32)
+              static_cast<float*>(a.C)[t * a.ldc + col] = acc[j] + bv;
+            else
+              static_cast<uint16_t*>(a.C)[t * a.ldc + col] =
+                  static_cast<uint16_t>(blk::pack2<kOut == blk::kOutBf16>(acc[j] + bv, 0.0f) & 0xffffu);
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+}  // namespace skinny
+}  // namespace i8

@@ -334,6 +334,125 @@ i8_status i8_igemm_s32(const int8_t* A, int64_t T, int64_t K, const int8_t* B, i
                        int32_t* acc, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Block-scaled e4m3: a linear layer whose codes have one fp32 scale for each block of 128,
+ * in place of one for each row.  A value far from its neighbours then costs range in its own
+ * block alone, so there is no outlier search and no fp16 product beside the codes' product.
+ * The format is that of checkpoints which keep e4m3 weights with a scale tensor of one entry
+ * per 128 x 128 tile (value = code * scale).
+ *
+ * Codes and scales.  A block is 128 consecutive features of one row (activations, gradients
+ * of outputs) or a 128 x 128 tile (weights); the last block of a row or column may be short.
+ * With a = max(largest |v| of the block, 2^-100):
+ *   code  = e4m3 rounding (nearest, ties to even) of fl32(v * fl32(448 / a))
+ *   scale = fl32(a * fl32(1 / 448))
+ * The largest |v| is taken over the values that are not NaN.  NaN gives the NaN code; in a
+ * block with an infinity that element's code is NaN and the scale is infinite, so that what is
+ * not finite in a row of X (or in a tile of W) makes that row (those columns) of the output
+ * NaN, and no others.
+ *
+ * dtype: the 16-bit type of X, bias, Y and of the gradients, I8_DTYPE_F16 or I8_DTYPE_BF16.
+ * Shapes: T, N, K > 0 and K % 16 == 0; N may be any number.  All pointers 16-byte aligned.
+ *
+ * i8_block_quantize_act(X, dtype, T, K, Xq, SX, stream):
+ *   Xq [T, K] codes, SX [ceil(K/128), T] scales (block-major: the T scales of a block of
+ *   features lie together).
+ * i8_block_quantize_weight(W, dtype, Z, N, K, CB, SCB, stream): Z weights one after another
+ *   (1 for a linear layer); CB [Z, N, K] codes, SCB [Z, ceil(N/128), ceil(K/128)] scales.
+ * i8_block_linear_forward(X, dtype, T, K, CB, SCB, bias, N, Y, workspace, bytes, stream):
+ *   Y[t,n] = round( sum_b SX[b,t] * SCB[n/128,b] * sum_{k in block b} Xq[t,k] CB[n,k] + bias[n] )
+ *   with the codes' values; X is quantised by the call.  A block's sum and the sum over the
+ *   blocks are fp32; one rounding to dtype at the end.  bias may be NULL.  workspace: at least
+ *   i8_block_linear_workspace_size(T, N, K) bytes, contents need no initialisation (calls
+ *   sharing it must be ordered on one stream).
+ *   T <= 128 streams the weight once over all SMs; more rows take 256 x 256 tiles.
+ * i8_block_linear_backward(dY, X, dtype, T, N, K, CB, SCB, dX, dW, db, workspace, bytes, stream):
+ *   the gradients of y = x W^T + b passed straight through the quantisation, for the outputs
+ *   that are not NULL:
+ *     dX [T, K] = q(dY) W'           q(dY): dY in row blocks; W' = CB * SCB (needs CB, SCB)
+ *     dW [N, K] = t(dY)^T t(X)       t(.): in 128 x 128 tiles (needs X)
+ *     db [N]    = sum_t dY[t]        summed in fp32 in a fixed order
+ *   all in dtype.  Products on e4m3 tensor cores, sums in fp32.  workspace: at least
+ *   i8_block_linear_backward_workspace_size(T, N, K) bytes.
+ * Errors as for the other calls: a violation returns I8_ERR_INVALID_ARG, nothing launched.
+ */
+enum { I8_DTYPE_F16 = 0, I8_DTYPE_BF16 = 1, I8_DTYPE_F32 = 2 };
+i8_status i8_block_quantize_act(const void* X, int32_t dtype, int64_t T, int64_t K, uint8_t* Xq,
+                                float* SX, void* stream);
+i8_status i8_block_quantize_weight(const void* W, int32_t dtype, int64_t Z, int64_t N, int64_t K,
+                                   uint8_t* CB, float* SCB, void* stream);
+size_t i8_block_linear_workspace_size(int64_t T, int64_t N, int64_t K);
+i8_status i8_block_linear_forward(const void* X, int32_t dtype, int64_t T, int64_t K,
+                                  const uint8_t* CB, const float* SCB, const void* bias, int64_t N,
+                                  void* Y, void* workspace, size_t workspace_bytes, void* stream);
+size_t i8_block_linear_backward_workspace_size(int64_t T, int64_t N, int64_t K);
+i8_status i8_block_linear_backward(const void* dY, const void* X, int32_t dtype, int64_t T,
+                                   int64_t N, int64_t K, const uint8_t* CB, const float* SCB,
+                                   void* dX, void* dW, void* db, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * Routing of tokens to experts.  For each token, with x its E logits (dtype F16, BF16 or F32):
+ *   p   = softmax(x) or sigmoid(x) (score: I8_SCORE_SOFTMAX, I8_SCORE_SIGMOID)
+ *   key = p + balance (balance [E] fp32 or NULL), -inf where x is -inf (a masked expert)
+ *   n_groups > 1: experts lie in n_groups equal runs; a run's total is the sum of its best two
+ *     keys (its best one without balance) among its unmasked members, -inf when it has none;
+ *     the experts outside the top_groups best runs get key -inf
+ *   the k experts of the largest keys, largest first, the lower index first among equals
+ *   weight = scale * p / sum of the chosen p (renormalize != 0; 0 when that sum is 0), or
+ *            scale * p
+ * weights [T, k] fp32, idx [T, k] int32.  A choice that finds no expert with a key above -inf
+ * has index -1 and weight 0.  Scores, keys and sums are held in 64 bits.  A NaN logit is never
+ * chosen and makes the weights of its token's choices NaN, as +inf does under softmax.
+ * E <= 512, k <= min(E, 32), n_groups <= 32 and a divisor of E.
+ *
+ * i8_route_experts_backward: dlogits [T, E] (dtype) from dweights [T, k] fp32 and the idx of the
+ * forward; the choice and the balance have no gradient.  An index >= E sets I8_ERR_DEVICE.
+ */
+enum { I8_SCORE_SOFTMAX = 0, I8_SCORE_SIGMOID = 1 };
+i8_status i8_route_experts(const void* logits, int32_t dtype, int64_t T, int64_t E,
+                           const float* balance, int32_t score, int64_t n_groups,
+                           int64_t top_groups, int64_t k, int32_t renormalize, float scale,
+                           float* weights, int32_t* idx, void* stream);
+i8_status i8_route_experts_backward(const void* logits, int32_t dtype, int64_t T, int64_t E,
+                                    int32_t score, int64_t k, int32_t renormalize, float scale,
+                                    const int32_t* idx, const float* dweights, void* dlogits,
+                                    void* stream);
+
+/*
+ * Experts: gated feed-forward layers with block-scaled e4m3 weights, each token through the k
+ * experts that its routing chose:
+ *   g = x W1^T, u = x W3^T, h = silu(g) * u        (W1, W3 [I, K] of expert idx[t,j])
+ *   Y[t] = round( sum_j weights[t,j] * (q(h) W2^T) )   (W2 [K, I]; q: row blocks of 128)
+ * x is quantised in row blocks.  g, u, h, the products and the sum over j (in the order of j)
+ * are fp32; Y [T, K] in dtype (F16 or BF16).
+ *   idx [T, k] int32: an expert, or negative for none (the term is left out); idx >= E is left
+ *     out too and sets I8_ERR_DEVICE.  weights [T, k] fp32.  An expert may appear twice.
+ *   CB13 [E, 2, I, K] codes (W1 then W3), S13 [E, 2, ceil(I/128), ceil(K/128)] scales,
+ *   CB2 [E, K, I], S2 [E, ceil(K/128), ceil(I/128)]: i8_block_quantize_weight with Z = 2E and E
+ *   GU [T * k, 2, I] fp32 or NULL: g and u, for the backward (in the library's own row order)
+ * Shapes: T, K, I > 0, K % 16 == 0, I % 16 == 0, E <= 512, k <= 32 (k may exceed E).
+ *
+ * i8_experts_backward: the experts are frozen; gradients of x and of the weights:
+ *   dh = q(dY) W2;  dweights[t,j] = sum_i dh_i h_i;  dX = sum_j ( q(dg) W1 + q(du) W3 ) with
+ *   dg, du the gradients of h = silu(g) * u times weights[t,j].  dX [T, K] in dtype, dweights
+ *   [T, k] fp32 (0 for a choice without an expert).  idx and weights as in the forward.
+ * workspace: at least i8_experts_workspace_size / i8_experts_backward_workspace_size bytes.
+ */
+size_t i8_experts_workspace_size(int64_t T, int64_t K, int64_t I, int64_t E, int64_t k);
+i8_status i8_experts_forward(const void* X, int32_t dtype, int64_t T, int64_t K,
+                             const int32_t* idx, const float* weights, int64_t k,
+                             const uint8_t* CB13, const float* S13, const uint8_t* CB2,
+                             const float* S2, int64_t E, int64_t I, void* Y, float* GU,
+                             void* workspace, size_t workspace_bytes, void* stream);
+size_t i8_experts_backward_workspace_size(int64_t T, int64_t K, int64_t I, int64_t E, int64_t k);
+i8_status i8_experts_backward(const void* dY, int32_t dtype, int64_t T, int64_t K,
+                              const int32_t* idx, const float* weights, int64_t k,
+                              const uint8_t* CB13, const float* S13, const uint8_t* CB2,
+                              const float* S2, int64_t E, int64_t I, const float* GU, void* dX,
+                              float* dweights, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
  * Synchronise `stream`, then read and clear the per-device error word.
  * Returns I8_ERR_CUDA if the stream reports an error, I8_ERR_TIMEOUT if a bounded wait
  * ran out, I8_ERR_DEVICE if a device-side check failed, else I8_OK.

@@ -19,12 +19,15 @@
 //
 // Design (sm_100a): persistent clusters of two CTAs, 256 x 256 output tiles,
 // tcgen05.mma.cta_group::2 kind::f8f6f4 (M = 256, N = 256, K = 32), a ring of six 32 KB stages
-// filled by TMA (no multicast).  Warps: 0 loads A and arms the leader's barrier, 2 loads B,
-// 1 allocates TMEM and (leader lane 0) issues the MMAs, 3 lays out the groups' tiles, 4..11
-// are the epilogue: warp w reads TMEM lanes 32*(w%4).. and columns 128*((w-4)/4)...
-// A thread's row is fixed and its 128 columns share one B scale, so a block costs it 128 FMAs
-// with one scalar factor.  The registers are split 72 / 208 between the first four warps and
-// the epilogue (setmaxnreg): 128 * 72 + 256 * 208 = 62,464 of the 64,512 the CTA starts with.
+// filled by TMA (no multicast).  Warps: 0 loads A and B and arms the leader's barrier,
+// 1 lays out the groups' tiles, allocates TMEM and (leader lane 0) issues the MMAs, 3 holds the
+// products of the scales ready in shared memory, 4..11 are the
+// epilogue: warp w reads TMEM lanes 32*(w%4).. and columns 128*((w-4)/4)...
+// A thread's row is fixed and its 128 columns share one B scale, so a block costs it 64 packed
+// FMAs (fma.rn.f32x2) with one scalar factor.  The registers are split 72 / 208 between the first
+// four warps and the epilogue (setmaxnreg): 128 * 72 + 256 * 208 = 62,464 of the 64,512 that the
+// CTA starts with.  With 128 sums a thread, 32 values on their way out of TMEM spilled in the
+// loop; two sets of 16, one loading while the other is added, do not.
 //
 // Gated form (kOut = kOutGated, an expert's first product): a tile holds 128 hidden features,
 // each CTA's 128 rows of B being 64 rows of the gate weight and the same 64 of the up weight,
@@ -48,20 +51,21 @@ constexpr int A_BYTES = HM * BK;
 constexpr int STAGE_BYTES = A_BYTES + HN * BK;
 constexpr int THREADS = 384;
 constexpr int EPI_WARP0 = 4;
+constexpr int REGS_LOW = 72, REGS_EPI = 208;
+constexpr int REGS_NEEDED = (128 * REGS_LOW + 256 * REGS_EPI + THREADS - 1) / THREADS;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int GROUP_M = 16;                   // m-tiles per raster group
 constexpr int MAX_GROUPS = 512;
 constexpr int CST_BYTES = 8 * 32 * 64;        // output staging: a 32 x 32 16-bit block a warp
 constexpr int AUX_BYTES = 2 * 2 * 128 * 4;    // bias of the tile's columns, or row maxima
 constexpr int PRE_BYTES = 2064;               // m-tiles before each group
-constexpr int BAR_BYTES = 256;
+constexpr int SLOTS = 8;                      // blocks whose scales are held ready
+constexpr int SCALE_BYTES = SLOTS * 2 * HM * 4;
+constexpr int BAR_BYTES = 512;
 constexpr size_t SMEM_BYTES = static_cast<size_t>(STAGES) * STAGE_BYTES + CST_BYTES + AUX_BYTES +
-                              PRE_BYTES + BAR_BYTES + 1024;
+                              PRE_BYTES + SCALE_BYTES + BAR_BYTES + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 static_assert(PRE_BYTES >= (MAX_GROUPS + 1) * 4, "group prefix");
-
-constexpr int REGS_LOW = 72, REGS_EPI = 208;
-constexpr int REGS_NEEDED = (128 * REGS_LOW + 256 * REGS_EPI + THREADS - 1) / THREADS;
 
 enum { kOutF16 = 0, kOutBf16 = 1, kOutF32 = 2, kOutGated = 3 };
 
@@ -91,9 +95,10 @@ struct GemmArgs {
 
 struct SmemBars {
   uint64_t full[STAGES];
-  uint64_t empty[STAGES];
-  uint64_t tmem_full[2];
+  uint64_t empty[STAGES];     // a block's MMAs are done: its stage is free, its sums are in TMEM
   uint64_t tmem_empty[2];
+  uint64_t scaled[SLOTS];     // the block's scales are in its slot
+  uint64_t unscaled[SLOTS];   // the epilogue is done with them
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -101,6 +106,51 @@ struct SmemBars {
 static_assert(sizeof(SmemBars) <= BAR_BYTES, "barrier block");
 
 __device__ __forceinline__ void epi_bar256() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Arrive on the pair leader's barrier, ordered as the reads of TMEM before it are (they have
+// completed: tcgen05.wait::ld, then the tcgen05 fence).  The release is at CTA scope: nothing in
+// memory is handed over, and a release at cluster scope waits for the thread's outstanding
+// memory operations every time (the warps' largest stall: 2.78 ms against X ms at
+// 2048 x 12288 x 49152).
+__device__ __forceinline__ void arrive_leader(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// 32 lanes x 16 consecutive 32-bit columns of TMEM into 16 registers; and the wait for it,
+// declared to produce them, so that no use comes before it.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_x16_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+        "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+        "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+      :
+      : "memory");
+}
+
+// two fp32 numbers in a register pair: the same value twice, and d * s + a of each
+__device__ __forceinline__ uint64_t pair2(float v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint32_t d0, uint32_t d1, uint64_t s, uint64_t a) {
+  uint64_t r;
+  asm("{\n\t.reg .b64 d;\n\t"
+      "mov.b64 d, {%1, %2};\n\t"
+      "fma.rn.f32x2 %0, d, %3, %4;\n\t}"
+      : "=l"(r) : "r"(d0), "r"(d1), "l"(s), "l"(a));
+  return r;
+}
 
 // every bulk store of this thread has read its shared-memory source
 __device__ __forceinline__ void bulk_wait_read_0() {
@@ -133,6 +183,39 @@ __device__ __forceinline__ void raster(int t, int m_tiles, int n_tiles, int& mt,
   nt = r / rows;
 }
 
+// Shared-memory descriptors of the 128-byte-swizzled operand tiles (K-major, and MN-major with
+// 128 elements of m or n in a row): the low word holds the address, the high word is the same
+// for every tile: 1024 bytes between groups of 8 rows, version 1, 128-byte swizzle.
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+template <bool kMN>
+__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr) {
+  return ((smem_addr & 0x3FFFFu) >> 4) | ((kMN ? (8192u >> 4) : 1u) << 16);
+}
+
+// D[tmem] (+)= A[smem] B[smem]^T over the CTA pair, issued by the lane with lead != 0.
+__device__ __forceinline__ void umma_lead(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                          uint32_t accumulate, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %6};\n\t"
+      "mov.b64 db, {%2, %6};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(lead), "r"(DESC_HI)
+      : "memory");
+}
+// The lead lane's MMAs so far done: one arrival on the barrier at `bar` of both CTAs.
+__device__ __forceinline__ void commit_lead(uint32_t bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;\n\t}" ::"r"(bar),
+      "h"(gemm::PAIR_MASK), "r"(lead)
+      : "memory");
+}
+
 template <bool kAMN, bool kBMN, int kOut>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     block_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
@@ -146,8 +229,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const uint32_t cstage = ring + static_cast<uint32_t>(STAGES * STAGE_BYTES);
   float* aux = reinterpret_cast<float*>(smem + static_cast<size_t>(STAGES) * STAGE_BYTES + CST_BYTES);
   int* pre = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(aux) + AUX_BYTES);
-  SmemBars* bars = reinterpret_cast<SmemBars*>(reinterpret_cast<uint8_t*>(pre) + PRE_BYTES);
-  const int warp = threadIdx.x >> 5;
+  float* slots = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(pre) + PRE_BYTES);
+  SmemBars* bars = reinterpret_cast<SmemBars*>(reinterpret_cast<uint8_t*>(slots) + SCALE_BYTES);
+  // the warp's number as one value for the warp: what follows from it stays in uniform registers
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   const uint32_t rank = gemm::cluster_rank();
   volatile int* abort_flag = &bars->abort_flag;
@@ -158,8 +243,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(smem_u32(&bars->empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_u32(&bars->tmem_full[b]), 1);
       mbar_init(smem_u32(&bars->tmem_empty[b]), 16);   // 8 epilogue warps x 2 CTAs
+    }
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(smem_u32(&bars->scaled[i]), 1);
+      mbar_init(smem_u32(&bars->unscaled[i]), 8);    // this CTA's epilogue warps
     }
     mbar_init(smem_u32(&bars->drain), 1);
     bars->abort_flag = 0;
@@ -176,7 +264,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
   grid_dep_wait();
   grid_dep_launch();
-  if (warp == 3) {
+  if (warp == 1) {
     // m-tiles before each group: every lane sums its run of groups, then a scan over lanes
     if (a.offsets == nullptr) {
       if (lane == 0) {
@@ -206,10 +294,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   __syncthreads();
   gemm::cluster_sync();
   tc_fence_after();
-  const uint32_t tmem_base = bars->tmem_base;
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
 
   const int KB = a.k_blocks;
-  const int num_tiles = pre[a.groups] * a.n_tiles;
+  const int num_tiles = __shfl_sync(0xffffffffu, pre[a.groups] * a.n_tiles, 0);
   const int cluster_id = blockIdx.x >> 1;
   const int num_clusters = gridDim.x >> 1;
   const uint64_t lim = a.wait_limit_ns;
@@ -234,10 +322,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
   if (warp < EPI_WARP0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_LOW));
-    if (warp == 0 || warp == 2) {
+    if (warp == 0) {
       if (lane == 0) {
-        // -------------------------------------------------------------- TMA producers
-        const bool loads_a = (warp == 0);
+        // -------------------------------------------------------------- TMA producer
         const uint32_t full_leader0 = gemm::map_to_rank(smem_u32(&bars->full[0]), 0);
         int s = 0;
         uint32_t ph = 0, issued = 0;
@@ -254,27 +341,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               ok = false;
               break;
             }
-            const uint32_t dst = ring + s * STAGE_BYTES + (loads_a ? 0u : static_cast<uint32_t>(A_BYTES));
-            if (loads_a && rank == 0)
-              mbar_arrive_expect_tx(smem_u32(&bars->full[s]), 2 * STAGE_BYTES);
+            const uint32_t da = ring + s * STAGE_BYTES, db = da + A_BYTES;
+            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&bars->full[s]), 2 * STAGE_BYTES);
             const uint32_t fb = full_leader0 + static_cast<uint32_t>(s) * 8u;
-            if (loads_a) {
-              if (kAMN)
-                gemm::tma_load_2d_pair(dst, &tmA, fb, m0, kb * BK);
-              else
-                gemm::tma_load_2d_pair(dst, &tmA, fb, kb * BK, m0);
-            } else if (kOut == kOutGated) {
+            if (kAMN)
+              gemm::tma_load_2d_pair(da, &tmA, fb, m0, kb * BK);
+            else
+              gemm::tma_load_2d_pair(da, &tmA, fb, kb * BK, m0);
+            if (kOut == kOutGated) {
               const int i0 = nt * HN + static_cast<int>(rank) * 64;
-              gemm::tma_load_3d_pair(dst, &tmB, fb, kb * BK, i0, z0);
-              gemm::tma_load_3d_pair(dst + 8192u, &tmB, fb, kb * BK, i0, z0 + 1);
+              gemm::tma_load_3d_pair(db, &tmB, fb, kb * BK, i0, z0);
+              gemm::tma_load_3d_pair(db + 8192u, &tmB, fb, kb * BK, i0, z0 + 1);
             } else if (kBMN) {
-              gemm::tma_load_3d_pair(dst, &tmB, fb, n0, kz * BK, z0 + zb);
+              gemm::tma_load_3d_pair(db, &tmB, fb, n0, kz * BK, z0 + zb);
               if (++kz == a.blocks_per_z) {
                 kz = 0;
                 ++zb;
               }
             } else {
-              gemm::tma_load_3d_pair(dst, &tmB, fb, kb * BK, n0, z0);
+              gemm::tma_load_3d_pair(db, &tmB, fb, kb * BK, n0, z0);
             }
             ++issued;
             if (++s == STAGES) {
@@ -283,7 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             }
           }
         }
-        if (!ok && loads_a && rank == 0) {
+        if (!ok && rank == 0) {
           // wind down: wait (bounded, ignoring the abort flag) for the copies in flight
           int no_abort = 0;
           const uint32_t inflight = issued < STAGES ? issued : STAGES;
@@ -294,33 +379,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
       }
     } else if (warp == 1) {
-      if (lane == 0 && rank == 0) {
+      if (rank == 0) {
         // -------------------------------------------------------------- MMA issuer
+        // The whole warp walks the loop, so that descriptors and addresses are uniform values;
+        // lane 0 alone issues.  (With one lane in the loop every MMA and commit took about 70
+        // cycles to issue, 600 to 780 a block against the 512 that its MMAs run.)
         constexpr uint32_t ID = idesc_e4m3_f32(TM, TN) | (kAMN ? (1u << 15) : 0u) | (kBMN ? (1u << 16) : 0u);
+        const uint32_t lead = lane == 0 ? 1u : 0u;
+        const uint32_t a0 = desc_lo<kAMN>(ring), b0 = desc_lo<kBMN>(ring + A_BYTES);
         int s = 0;
         uint32_t ph = 0, n = 0;                     // n: blocks issued so far
         bool ok = true;
         for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
           for (int kb = 0; kb < KB; ++kb, ++n) {
             const uint32_t b = n & 1u;
-            if (!mbar_wait(smem_u32(&bars->tmem_empty[b]), ((n >> 1) & 1u) ^ 1u, abort_flag, lim) ||
-                !mbar_wait(smem_u32(&bars->full[s]), ph, abort_flag, lim)) {
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->tmem_empty[b]), ((n >> 1) & 1u) ^ 1u, abort_flag, lim) &&
+                                             mbar_wait(smem_u32(&bars->full[s]), ph, abort_flag, lim))) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t sa = ring + s * STAGE_BYTES;
-            const uint32_t sb = sa + A_BYTES;
-            const uint32_t d = tmem_base + b * TN;
+            const uint32_t so = static_cast<uint32_t>(s) * (STAGE_BYTES >> 4);
 #pragma unroll
-            for (int kk = 0; kk < BK / 32; ++kk) {
+            for (int kk = 0; kk < BK / 32; ++kk)
               // 32 terms further: 32 bytes along a K-major row, 32 rows of 128 bytes otherwise
-              const uint64_t ad = kAMN ? bwd::sdesc_mn_sw128(sa + kk * 4096) : sdesc_k_sw128(sa + kk * 32);
-              const uint64_t bd = kBMN ? bwd::sdesc_mn_sw128(sb + kk * 4096) : sdesc_k_sw128(sb + kk * 32);
-              gemm::umma_e4m3_pair(d, ad, bd, ID, kk != 0);
-            }
-            gemm::umma_commit_pair(smem_u32(&bars->empty[s]));
-            gemm::umma_commit_pair(smem_u32(&bars->tmem_full[b]));
+              umma_lead(tmem_base + b * TN, a0 + so + kk * (kAMN ? 256 : 2), b0 + so + kk * (kBMN ? 256 : 2), ID,
+                        kk != 0, lead);
+            commit_lead(smem_u32(&bars->empty[s]), lead);
             if (++s == STAGES) {
               s = 0;
               ph ^= 1u;
@@ -328,8 +413,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
         }
         int no_abort = 0;
-        gemm::umma_commit_pair(smem_u32(&bars->drain));
+        commit_lead(smem_u32(&bars->drain), lead);
         mbar_wait(smem_u32(&bars->drain), 0u, &no_abort, lim);
+      }
+    } else if (warp == 3) {
+      // ---------------------------------------------------------------- scales
+      // SA * SB of every block, for the 128 rows of this CTA and both halves of the columns (gate
+      // and up in the gated form), into one of SLOTS slots.  The epilogue has no load of its own
+      // in its loop: with the loads there, one block ahead, it took 888 cycles a block, with
+      // constants in their place 740.
+      constexpr int AHEAD = 4;                      // blocks loaded together
+      uint32_t n = 0;                               // blocks so far
+      bool ok = true;
+      for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
+        int g, row0, row_end, nt;
+        tile_at(t, g, row0, row_end, nt);
+        const int r0 = row0 + static_cast<int>(rank) * HM + lane;
+        const float* sb0 = a.SB + g * a.sb_group;
+        const float* sb1;
+        if (kOut == kOutGated) {
+          sb0 += nt * a.sb_col;
+          sb1 = sb0 + (a.sb_group >> 1);
+        } else {
+          const int c1 = nt * TN + HN < a.Nc ? 2 * nt + 1 : 2 * nt;   // a half past the last column: any scale
+          sb1 = sb0 + c1 * a.sb_col;
+          sb0 += 2 * nt * a.sb_col;
+        }
+        int64_t ra[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ra[i] = min(r0 + 32 * i, a.M - 1) >> a.sa_shift;
+        for (int k0 = 0; k0 < KB && ok; k0 += AHEAD) {
+          float va[AHEAD][4], vb[AHEAD][2];
+#pragma unroll
+          for (int u = 0; u < AHEAD; ++u)
+            if (k0 + u < KB) {
+              const float* p = a.SA + static_cast<int64_t>(k0 + u) * a.sa_pitch;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) va[u][i] = __ldg(p + ra[i]);
+              vb[u][0] = __ldg(sb0 + (k0 + u) * a.sb_block);
+              vb[u][1] = __ldg(sb1 + (k0 + u) * a.sb_block);
+            }
+#pragma unroll
+          for (int u = 0; u < AHEAD; ++u) {
+            if (k0 + u >= KB || !ok) break;
+            const uint32_t slot = n & (SLOTS - 1);
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->unscaled[slot]), ((n / SLOTS) & 1u) ^ 1u, abort_flag, lim));
+            if (!ok) break;
+            float* dst = slots + slot * (2 * HM) + lane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              dst[32 * i] = va[u][i] * vb[u][0];
+              dst[HM + 32 * i] = va[u][i] * vb[u][1];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->scaled[slot]));
+            ++n;
+          }
+        }
       }
     }
   } else {
@@ -342,6 +482,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t cst = cstage + static_cast<uint32_t>((warp - EPI_WARP0) * 2048);
     const uint32_t empty_leader0 = gemm::map_to_rank(smem_u32(&bars->tmem_empty[0]), 0);
     uint32_t n = 0;
+    int s = 0;                                      // the block's ring stage, as the issuer's
+    uint32_t ph = 0;
     int parity = 0;
     // after a wait that ran out, a warp keeps walking the tiles (it must meet the others at
     // the named barrier) but touches TMEM and memory no more
@@ -361,54 +503,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         aux[parity * 256 + et] = bv;
         epi_bar256();
       }
-      const float* sa = a.SA + ((row < a.M ? row : a.M - 1) >> a.sa_shift);
-      const float* sb0;
-      const float* sb1 = nullptr;
-      if (kOut == kOutGated) {
-        sb0 = a.SB + g * a.sb_group + nt * a.sb_col;
-        sb1 = sb0 + (a.sb_group >> 1);
-      } else {
-        const int cb = n0 < a.Nc ? n0 >> 7 : 0;     // a half past the last column: any scale
-        sb0 = a.SB + g * a.sb_group + cb * a.sb_col;
-      }
-      float acc[128];
+      // sums of the thread's 128 columns, two to a register pair (fma.rn.f32x2)
+      uint64_t acc2[64];
 #pragma unroll
-      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
-      float s0 = 0.0f, s1 = 0.0f;
-      if (!dead) {
-        const float v = __ldg(sa);
-        s0 = v * __ldg(sb0);
-        if (kOut == kOutGated) s1 = v * __ldg(sb1);
-      }
+      for (int j = 0; j < 64; ++j) acc2[j] = 0ull;
       for (int kb = 0; kb < KB && !dead; ++kb, ++n) {
         const uint32_t b = n & 1u;
-        float s0n = 0.0f, s1n = 0.0f;               // the next block's scales, ahead of the wait
-        if (kb + 1 < KB) {
-          const float v = __ldg(sa + static_cast<int64_t>(kb + 1) * a.sa_pitch);
-          s0n = v * __ldg(sb0 + static_cast<int64_t>(kb + 1) * a.sb_block);
-          if (kOut == kOutGated) s1n = v * __ldg(sb1 + static_cast<int64_t>(kb + 1) * a.sb_block);
-        }
-        const bool got = mbar_wait(smem_u32(&bars->tmem_full[b]), (n >> 1) & 1u, abort_flag, lim);
+        const bool got = mbar_wait(smem_u32(&bars->scaled[n & (SLOTS - 1)]), (n / SLOTS) & 1u, abort_flag, lim) &&
+                         mbar_wait(smem_u32(&bars->empty[s]), ph, abort_flag, lim);
+        const float* sc = slots + (n & (SLOTS - 1)) * (2 * HM) + q * 32 + lane;
+        const uint64_t s0 = pair2(sc[kOut == kOutGated ? 0 : half * HM]);
+        const uint64_t s1 = kOut == kOutGated ? pair2(sc[HM]) : s0;
         if (!__all_sync(0xffffffffu, got)) {
           dead = true;
           break;
         }
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
         tc_fence_after();
         const uint32_t tb = lane_base + b * TN;
+        // 16 columns at a time: the next 16 are on their way while these are added
+        uint32_t r[2][16];
+        tmem_ld_x16(tb, r[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(tb + static_cast<uint32_t>(c * 32), r);
-          tmem_ld_wait_regs(r);
-          const float s = (kOut == kOutGated && c >= 2) ? s1 : s0;
+        for (int c = 0; c < 8; ++c) {
+          tmem_ld_x16_wait(r[c & 1]);
+          if (c < 7) tmem_ld_x16(tb + static_cast<uint32_t>((c + 1) * 16), r[(c + 1) & 1]);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) acc[c * 32 + j] = fmaf(__uint_as_float(r[j]), s, acc[c * 32 + j]);
+          for (int j = 0; j < 8; ++j)
+            acc2[c * 8 + j] = fma2(r[c & 1][2 * j], r[c & 1][2 * j + 1], c >= 4 ? s1 : s0, acc2[c * 8 + j]);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) gemm::mbar_arrive_remote(empty_leader0 + b * 8u);
-        s0 = s0n;
-        s1 = s1n;
+        if (lane == 0) {
+          arrive_leader(empty_leader0 + b * 8u);
+          mbar_arrive(smem_u32(&bars->unscaled[n & (SLOTS - 1)]));
+        }
+      }
+      float acc[128];
+#pragma unroll
+      for (int j = 0; j < 64; ++j) {
+        acc[2 * j] = __uint_as_float(static_cast<uint32_t>(acc2[j]));
+        acc[2 * j + 1] = __uint_as_float(static_cast<uint32_t>(acc2[j] >> 32));
       }
       if (kOut == kOutGated) {
         // acc[0..63] = g, acc[64..127] = u of features i0 .. i0 + 63

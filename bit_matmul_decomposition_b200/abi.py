@@ -8,6 +8,7 @@ A missing or unloadable library raises; nothing here falls back to another compu
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -110,25 +111,31 @@ def _check(fn, code):
 def _ptr(t) -> Optional[int]:
     if t is None:
         return None
-    if not t.is_cuda:
+    index = t.get_device()                  # -1 for a CPU tensor
+    if index < 0:
         raise ValueError("expected a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
-    import torch
-    if t.device.index != torch.cuda.current_device():
+    current = _torch()._C._cuda_getDevice()
+    if index != current:
         raise ValueError("tensor on %s, but the current device is cuda:%d: the call would "
-                         "launch there (use torch.cuda.device)"
-                         % (t.device, torch.cuda.current_device()))
+                         "launch there (use torch.cuda.device)" % (t.device, current))
     return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=None)
+def _torch():
+    import torch
+    return torch
 
 
 # The C calls take bare pointers, and most buffers have no size argument: the library
 # trusts that X is [T, K], C is [T, N], and so on.  These checks hold every tensor to the
 # dtype and the element count that its header comment states, so that a wrong or short
 # buffer raises here instead of being read or written out of bounds on the device.
+@functools.lru_cache(maxsize=None)
 def _dt(*names):
-    import torch
-    return tuple(getattr(torch, n) for n in names)
+    return tuple(getattr(_torch(), n) for n in names)
 
 
 def _arg(t, name, dtypes, elems):
@@ -184,9 +191,9 @@ def _check_act_outputs(T, K, col_mask, mask_words, outlier_idx, n_outliers, Xq, 
 
 
 def _stream(stream):
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:                      # the current stream's handle
+        C = _torch()._C
+        return C._cuda_getCurrentRawStream(C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -377,13 +384,17 @@ def i8_dequantize_weight(CB, SCB, W, stream=None):
 SCORES = {"softmax": 0, "sigmoid": 1}
 
 
+@functools.lru_cache(maxsize=None)
+def _type_codes():
+    torch = _torch()
+    return {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
 def _dtype16(t, name):
     """The header's code of a 16-bit floating-point tensor's type."""
-    import torch
-    if t is not None and t.dtype == torch.float16:
-        return 0
-    if t is not None and t.dtype == torch.bfloat16:
-        return 1
+    code = 2 if t is None else _type_codes().get(t.dtype, 2)
+    if code < 2:
+        return code
     raise TypeError("%s: dtype %s, expected torch.float16 or torch.bfloat16"
                     % (name, None if t is None else t.dtype))
 
@@ -426,6 +437,7 @@ def i8_block_quantize_weight(W, CB, SCB, stream=None):
                                            _stream(stream)))
 
 
+@functools.lru_cache(maxsize=1024)
 def i8_block_linear_workspace_size(T, N, K) -> int:
     return int(load().i8_block_linear_workspace_size(T, N, K))
 
@@ -452,6 +464,7 @@ def i8_block_linear_forward(X, CB, SCB, bias, Y, workspace, stream=None):
                                           _stream(stream)))
 
 
+@functools.lru_cache(maxsize=1024)
 def i8_block_linear_backward_workspace_size(T, N, K) -> int:
     return int(load().i8_block_linear_backward_workspace_size(T, N, K))
 
@@ -487,14 +500,11 @@ def i8_block_linear_backward(dY, X, CB, SCB, dX, dW, db, workspace, stream=None)
 
 
 def _logits(t):
-    import torch
-    if t is not None and t.dtype == torch.float32:
-        return 2
-    try:
-        return _dtype16(t, "logits")
-    except TypeError:
+    code = None if t is None else _type_codes().get(t.dtype)
+    if code is None:
         raise TypeError("logits: dtype %s, expected torch.float32, torch.float16 or "
-                        "torch.bfloat16" % (None if t is None else t.dtype)) from None
+                        "torch.bfloat16" % (None if t is None else t.dtype))
+    return code
 
 
 def i8_route_experts(logits, balance, score, n_groups, top_groups, k, renormalize, scale,
@@ -546,6 +556,7 @@ def _check_experts(X, name, idx, weights, CB13, S13, CB2, S2):
     return code, T, K, k, E, I
 
 
+@functools.lru_cache(maxsize=1024)
 def i8_experts_workspace_size(T, K, I, E, k) -> int:
     return int(load().i8_experts_workspace_size(T, K, I, E, k))
 
@@ -563,6 +574,7 @@ def i8_experts_forward(X, idx, weights, CB13, S13, CB2, S2, Y, GU, workspace, st
                                      _stream(stream)))
 
 
+@functools.lru_cache(maxsize=1024)
 def i8_experts_backward_workspace_size(T, K, I, E, k) -> int:
     return int(load().i8_experts_backward_workspace_size(T, K, I, E, k))
 

@@ -17,19 +17,30 @@ that trains its 16-bit weight dW = t(dy)^T t(x) in 128 x 128 tiles, db = sum(dy)
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Iterable, Optional, Tuple
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import abi
 
 DTYPES = (torch.float16, torch.bfloat16)
 
 
+def _on(device: torch.device):
+    """Makes `device` current, for the library launches there; nothing where it is already."""
+    if device.index == torch.cuda.current_device():
+        return _HERE
+    return torch.cuda.device(device)
+
+
+_HERE = contextlib.nullcontext()
+
+
 def _dense(t: torch.Tensor) -> torch.Tensor:
     """Contiguous and on a 16-byte boundary, as the library takes its pointers."""
-    t = t.contiguous()
+    if not t.is_contiguous():
+        t = t.contiguous()
     return t.clone() if t.data_ptr() % 16 else t
 
 
@@ -52,10 +63,9 @@ def quantize_weight_blocks(weight: torch.Tensor) -> Tuple[torch.Tensor, torch.Te
         raise TypeError("the weight must be fp16 or bf16 (got %s)" % weight.dtype)
     w = _dense(weight.detach())
     N, K = w.shape[-2:]
-    codes = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
-    scales = torch.empty((*w.shape[:-2], (N + 127) // 128, (K + 127) // 128),
-                         dtype=torch.float32, device=w.device)
-    with torch.cuda.device(w.device):
+    codes = w.new_empty(w.shape, dtype=torch.uint8)
+    scales = w.new_empty((*w.shape[:-2], (N + 127) // 128, (K + 127) // 128), dtype=torch.float32)
+    with _on(w.device):
         abi.i8_block_quantize_weight(w, codes, scales)
     return codes, scales
 
@@ -63,28 +73,26 @@ def quantize_weight_blocks(weight: torch.Tensor) -> Tuple[torch.Tensor, torch.Te
 def _forward(x2, codes, scales, bias):
     T, K = x2.shape
     N = codes.shape[0]
-    y = torch.empty((T, N), dtype=x2.dtype, device=x2.device)
+    y = x2.new_empty((T, N))
     if T > 0:
         # the workspace is the caching allocator's: ordered by the stream, and a graph that is
         # being captured gets one of its own
-        ws = torch.empty((abi.i8_block_linear_workspace_size(T, N, K),), dtype=torch.uint8,
-                         device=x2.device)
-        with torch.cuda.device(x2.device):
+        ws = codes.new_empty(abi.i8_block_linear_workspace_size(T, N, K), dtype=torch.uint8)
+        with _on(x2.device):
             abi.i8_block_linear_forward(x2, codes, scales, bias, y, ws)
     return y
 
 
 def _backward(gy, x2, codes, scales, K, want_x, want_w, want_b, dtype):
-    gy = _dense(gy.to(dtype))
+    gy = _dense(gy if gy.dtype == dtype else gy.to(dtype))
     T, N = gy.shape
-    new = torch.zeros if T == 0 else torch.empty
-    gx = new((T, K), dtype=dtype, device=gy.device) if want_x else None
-    gw = new((N, K), dtype=dtype, device=gy.device) if want_w else None
-    gb = new((N,), dtype=dtype, device=gy.device) if want_b else None
+    new = gy.new_zeros if T == 0 else gy.new_empty
+    gx = new((T, K)) if want_x else None
+    gw = new((N, K)) if want_w else None
+    gb = new((N,)) if want_b else None
     if T > 0 and (want_x or want_w or want_b):
-        ws = torch.empty((abi.i8_block_linear_backward_workspace_size(T, N, K),),
-                         dtype=torch.uint8, device=gy.device)
-        with torch.cuda.device(gy.device):
+        ws = gy.new_empty(abi.i8_block_linear_backward_workspace_size(T, N, K), dtype=torch.uint8)
+        with _on(gy.device):
             abi.i8_block_linear_backward(gy, x2, codes, scales, gx, gw, gb, ws)
     return gx, gw, gb
 
@@ -99,7 +107,6 @@ class _BlockLinearFn(torch.autograd.Function):
         return _forward(x2, codes, scales, bias)
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, gy):
         codes, scales = ctx.saved_tensors
         gx, _, gb = _backward(gy, None, codes, scales, codes.shape[1], ctx.needs_input_grad[0],
@@ -117,7 +124,6 @@ class _BlockLinearTrainFn(torch.autograd.Function):
         return _forward(x2, codes, scales, bias)
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, gy):
         x2, codes, scales = ctx.saved_tensors
         return _backward(gy, x2, codes, scales, codes.shape[1], *ctx.needs_input_grad, x2.dtype)
@@ -130,12 +136,12 @@ def linear_block_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     if codes.dim() != 2:
         raise ValueError("codes: a 2-D tensor is required")
     _check_input(x, codes.shape[1], codes.device)
-    x2 = _dense(x.reshape(-1, codes.shape[1]))
+    x2 = _dense(x if x.dim() == 2 else x.reshape(-1, codes.shape[1]))
     if torch.is_grad_enabled() and (x2.requires_grad or (bias is not None and bias.requires_grad)):
         y = _BlockLinearFn.apply(x2, codes, scales, bias)
     else:
         y = _forward(x2, codes, scales, bias)
-    return y.view(*x.shape[:-1], codes.shape[0])
+    return y if x.dim() == 2 else y.view(*x.shape[:-1], codes.shape[0])
 
 
 def linear_block_fp8_train(x: torch.Tensor, weight: torch.Tensor,
@@ -147,8 +153,9 @@ def linear_block_fp8_train(x: torch.Tensor, weight: torch.Tensor,
     _check_input(x, weight.shape[1], weight.device)
     if weight.dtype != x.dtype:
         raise TypeError("weight is %s, input %s: one type is required" % (weight.dtype, x.dtype))
-    y = _BlockLinearTrainFn.apply(_dense(x.reshape(-1, weight.shape[1])), weight, bias)
-    return y.view(*x.shape[:-1], weight.shape[0])
+    x2 = _dense(x if x.dim() == 2 else x.reshape(-1, weight.shape[1]))
+    y = _BlockLinearTrainFn.apply(x2, weight, bias)
+    return y if x.dim() == 2 else y.view(*x.shape[:-1], weight.shape[0])
 
 
 class LinearBlockFp8(torch.nn.Module):

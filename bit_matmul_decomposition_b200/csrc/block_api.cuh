@@ -34,18 +34,26 @@ BlockGemmFn block_gemm_fn(bool amn, bool bmn, int out) {
                              : blk::block_gemm_kernel<true, true, blk::kOutBf16>;
 }
 
+// the streaming product: tiles of 16 tokens form their codes themselves, larger ones take the
+// quantiser's
 template <int NT>
 SkinnyFn skinny_fn_nt(int out) {
+  using namespace skinny;
   switch (out) {
-    case blk::kOutF16: return skinny::block_skinny_kernel<NT, blk::kOutF16>;
-    case blk::kOutBf16: return skinny::block_skinny_kernel<NT, blk::kOutBf16>;
-    default: return skinny::block_skinny_kernel<NT, blk::kOutF32>;
+    case blk::kOutF16: return block_skinny_kernel<NT, blk::kOutF16, kInCodes>;
+    case blk::kOutBf16: return block_skinny_kernel<NT, blk::kOutBf16, kInCodes>;
+    default: return block_skinny_kernel<NT, blk::kOutF32, kInCodes>;
   }
 }
 
-SkinnyFn skinny_fn(int nt, int out) {
+SkinnyFn skinny_fn(int nt, int out, int in) {
+  using namespace skinny;
+  if (in == kInGated) return block_skinny_kernel<16, blk::kOutF32, kInGated>;
+  if (in == kInF16)
+    return out == blk::kOutF32 ? block_skinny_kernel<16, blk::kOutF32, kInF16> : block_skinny_kernel<16, blk::kOutF16, kInF16>;
+  if (in == kInBf16)
+    return out == blk::kOutF32 ? block_skinny_kernel<16, blk::kOutF32, kInBf16> : block_skinny_kernel<16, blk::kOutBf16, kInBf16>;
   switch (nt) {
-    case 16: return skinny_fn_nt<16>(out);
     case 32: return skinny_fn_nt<32>(out);
     case 64: return skinny_fn_nt<64>(out);
     default: return skinny_fn_nt<128>(out);
@@ -93,11 +101,16 @@ i8_status block_info(const DeviceInfo& d, BlockInfo** out) {
       if (c < 1) return I8_ERR_UNSUPPORTED;
       clusters = clusters == 0 || c < clusters ? c : clusters;
     }
-    for (int nt = 16; nt <= 128; nt *= 2)
-      for (int o = blk::kOutF16; o <= blk::kOutF32; ++o)
-        if (!cuda_ok(cudaFuncSetAttribute(skinny_fn(nt, o), smem_attr, static_cast<int>(skinny::smem_bytes(nt))),
+    for (int o = blk::kOutF16; o <= blk::kOutF32; ++o) {
+      for (int nt = 32; nt <= 128; nt *= 2)
+        if (!cuda_ok(cudaFuncSetAttribute(skinny_fn(nt, o, skinny::kInCodes), smem_attr, static_cast<int>(skinny::smem_bytes(nt))),
                      "cudaFuncSetAttribute(block skinny)"))
           return I8_ERR_CUDA;
+      for (int in = skinny::kInF16; in <= skinny::kInGated; ++in)
+        if (!cuda_ok(cudaFuncSetAttribute(skinny_fn(16, o, in), smem_attr, static_cast<int>(skinny::smem_bytes(16))),
+                     "cudaFuncSetAttribute(block skinny)"))
+          return I8_ERR_CUDA;
+    }
     b.clusters = clusters;
     b.init = true;
   }
@@ -167,7 +180,7 @@ i8_status run_block_gemm(bool amn, bool bmn, int out, const CUtensorMap& tA, con
   return cuda_ok(e, "kernel launch") ? launch_status() : I8_ERR_CUDA;
 }
 
-i8_status run_skinny(int nt, int out, const CUtensorMap& tW, const CUtensorMap& tX, skinny::Args a,
+i8_status run_skinny(int nt, int out, int in, const CUtensorMap& tW, const CUtensorMap& tX, skinny::Args a,
                      int64_t token_tiles, const DeviceInfo& d, cudaStream_t s) {
   a.wait_limit_ns = kWaitLimitNs;
   const int64_t tiles = token_tiles * a.n_tiles;
@@ -175,7 +188,7 @@ i8_status run_skinny(int nt, int out, const CUtensorMap& tW, const CUtensorMap& 
   const int64_t units = tiles * a.k_blocks;
   int64_t grid = d.sms < kPartGrid ? d.sms : kPartGrid;
   if (units < grid) grid = units;
-  const cudaError_t e = launch_overlapped(skinny_fn(nt, out), dim3(static_cast<unsigned>(grid)), dim3(skinny::THREADS),
+  const cudaError_t e = launch_overlapped(skinny_fn(nt, out, in), dim3(static_cast<unsigned>(grid)), dim3(skinny::threads(in)),
                                           skinny::smem_bytes(nt), s, tW, tX, a);
   return cuda_ok(e, "kernel launch") ? launch_status() : I8_ERR_CUDA;
 }
@@ -199,8 +212,10 @@ struct LinearWs {
 LinearWs linear_ws(int64_t T, int64_t K) {
   LinearWs w{};
   Taker take;
-  w.xq = take(T * K);
-  w.sx = take(blocks128(K) * T * 4);
+  if (T > 16) {
+    w.xq = take(T * K);
+    w.sx = take(blocks128(K) * T * 4);
+  }
   if (T <= kSkinnyMaxT) {
     w.arrived = take(kPartGrid * 4);
     w.parts = take(static_cast<int64_t>(parts_bytes(skinny_tokens(T))));
@@ -216,7 +231,8 @@ i8_status block_linear_forward(const void* X, int32_t dtype, int64_t T, int64_t 
   i8_status st = block_info(d, &b);
   if (st != I8_OK) return st;
   const LinearWs w = linear_ws(T, K);
-  const bool few = T <= kSkinnyMaxT;
+  const bool few = T <= kSkinnyMaxT, direct = T <= 16;
+  const bool bf = dtype == I8_DTYPE_BF16;
   blk::QuantArgs q = quant_args(X, T, K);
   q.Qr = ws + w.xq;
   q.qr_pitch = K;
@@ -226,15 +242,27 @@ i8_status block_linear_forward(const void* X, int32_t dtype, int64_t T, int64_t 
     q.zero = reinterpret_cast<unsigned int*>(ws + w.arrived);
     q.zero_words = kPartGrid;
   }
-  st = run_block_quant(dtype, q, 1, false, s);
+  // Neither kernel is launched with programmatic serialization: the product that follows may
+  // read the weight (and, direct, X) from its start, so what wrote them has to be done by then.
+  if (direct) {
+    skinny::clear_kernel<<<1, kPartGrid, 0, s>>>(q.zero);
+    st = launch_status();
+  } else {
+    st = run_block_quant(dtype, q, 1, false, s);
+  }
   if (st != I8_OK) return st;
-  const int out = dtype == I8_DTYPE_BF16 ? blk::kOutBf16 : blk::kOutF16;
+  const int out = bf ? blk::kOutBf16 : blk::kOutF16;
   const int KB = static_cast<int>(blocks128(K));
   CUtensorMap tX, tW;
   if (few) {
     const int nt = skinny_tokens(T);
-    if (!map_codes(&tW, CB, K, N, 1, K, skinny::ROWS) || !map_codes(&tX, ws + w.xq, K, T, 0, K, nt)) return I8_ERR_CUDA;
+    const int in = !direct ? skinny::kInCodes : bf ? skinny::kInBf16 : skinny::kInF16;
+    if (!map_codes(&tW, CB, K, N, 1, K, skinny::ROWS)) return I8_ERR_CUDA;
+    tX = tW;
+    if (!direct && !map_codes(&tX, ws + w.xq, K, T, 0, K, nt)) return I8_ERR_CUDA;
     skinny::Args a = {};
+    a.X = X;
+    a.k_cols = K;
     a.M = static_cast<int>(T);
     a.k_blocks = KB;
     a.n_tiles = a.n_per_z = static_cast<int>(blocks128(N));
@@ -248,7 +276,7 @@ i8_status block_linear_forward(const void* X, int32_t dtype, int64_t T, int64_t 
     a.ldc = N;
     a.parts = reinterpret_cast<float*>(ws + w.parts);
     a.arrived = reinterpret_cast<unsigned int*>(ws + w.arrived);
-    return run_skinny(nt, out, tW, tX, a, 1, d, s);
+    return run_skinny(nt, out, in, tW, tX, a, 1, d, s);
   }
   if (!map_codes(&tW, CB, K, N, 1, K, blk::HN) || !map_codes(&tX, ws + w.xq, K, T, 0, K, blk::HM)) return I8_ERR_CUDA;
   blk::GemmArgs a = {};
@@ -426,16 +454,21 @@ ExpertsWs experts_ws(const ExpertsShape& x, bool backward) {
   w.offsets = take((x.E + 1) * 4);
   w.place = take(x.R * 4);
   w.row_at = take(x.R * 4);
-  w.xq = take(x.R * x.K);                      // rows of x, or of dy, by expert
-  w.sx = take(static_cast<int64_t>(x.KB) * x.R * 4);
+  const bool direct = !backward && nt == 16;
+  if (!direct) {
+    w.xq = take(x.R * x.K);                    // rows of x, or of dy, by expert
+    w.sx = take(static_cast<int64_t>(x.KB) * x.R * 4);
+  }
   w.arrived = take(2 * kPartGrid * 4);
   if (!backward && nt > 0) {
     w.parts = take(static_cast<int64_t>(parts_bytes(nt)));
     w.gu = take(x.R * 2 * x.I * 4);
   }
   if (backward) w.gu = take(x.R * x.I * 4);    // dy W2
-  w.h = take(x.R * x.Ip * (backward ? 2 : 1));
-  w.sh = take(static_cast<int64_t>(x.IB) * x.R * 4 * (backward ? 2 : 1));
+  if (!direct) {
+    w.h = take(x.R * x.Ip * (backward ? 2 : 1));
+    w.sh = take(static_cast<int64_t>(x.IB) * x.R * 4 * (backward ? 2 : 1));
+  }
   w.y = take(x.R * x.K * 4);
   w.total = take.off;
   return w;
@@ -443,13 +476,13 @@ ExpertsWs experts_ws(const ExpertsShape& x, bool backward) {
 
 // groups the rows by expert and lays the codes of X's rows out in that order
 i8_status experts_rows(const void* X, int32_t dtype, const int32_t* idx, const ExpertsShape& x, const ExpertsWs& w,
-                       uint8_t* ws, float* dw, cudaStream_t s) {
+                       uint8_t* ws, float* dw, bool codes, cudaStream_t s) {
   int32_t* place = reinterpret_cast<int32_t*>(ws + w.place);
   moe::sort_rows_kernel<<<static_cast<unsigned>(x.E), moe::kSortThreads, 0, s>>>(
       idx, x.R, static_cast<int>(x.E), reinterpret_cast<int32_t*>(ws + w.offsets), place,
-      reinterpret_cast<int32_t*>(ws + w.row_at), dw);
+      reinterpret_cast<int32_t*>(ws + w.row_at), dw, reinterpret_cast<unsigned int*>(ws + w.arrived), 2 * kPartGrid);
   i8_status st = launch_status();
-  if (st != I8_OK) return st;
+  if (st != I8_OK || !codes) return st;
   blk::QuantArgs q = quant_args(X, x.T, x.K);
   q.Qr = ws + w.xq;
   q.qr_pitch = x.K;
@@ -457,8 +490,6 @@ i8_status experts_rows(const void* X, int32_t dtype, const int32_t* idx, const E
   q.rows_out = x.R;
   q.dest = place;
   q.copies = static_cast<int>(x.k);
-  q.zero = reinterpret_cast<unsigned int*>(ws + w.arrived);
-  q.zero_words = 2 * kPartGrid;
   return run_block_quant(dtype, q, 1, true, s);
 }
 
@@ -479,10 +510,11 @@ i8_status experts_forward(const void* X, int32_t dtype, const int32_t* idx, cons
   i8_status st = block_info(d, &b);
   if (st != I8_OK) return st;
   const ExpertsWs w = experts_ws(x, false);
-  st = experts_rows(X, dtype, idx, x, w, ws, nullptr, s);
+  const int nt = experts_tokens(x);
+  const bool direct = nt == 16;                // the products form the codes of their rows
+  st = experts_rows(X, dtype, idx, x, w, ws, nullptr, !direct, s);
   if (st != I8_OK) return st;
   const int32_t* offsets = reinterpret_cast<const int32_t*>(ws + w.offsets);
-  const int nt = experts_tokens(x);
   const int M = static_cast<int>(x.R), E = static_cast<int>(x.E);
   float* SX = reinterpret_cast<float*>(ws + w.sx);
   float* SH = reinterpret_cast<float*>(ws + w.sh);
@@ -492,10 +524,16 @@ i8_status experts_forward(const void* X, int32_t dtype, const int32_t* idx, cons
   if (nt > 0) {
     float* gu = GU != nullptr ? GU : reinterpret_cast<float*>(ws + w.gu);
     const int64_t token_tiles = x.R / nt + (x.R < x.E ? x.R : x.E);   // at most
-    if (!map_codes(&tX, ws + w.xq, x.K, x.R, 0, x.K, nt) || !map_codes(&tW13, CB13, x.K, x.I, 2 * x.E, x.K, skinny::ROWS) ||
-        !map_codes(&tH, ws + w.h, x.Ip, x.R, 0, x.Ip, nt) || !map_codes(&tW2, CB2, x.I, x.K, x.E, x.I, skinny::ROWS))
+    if (!map_codes(&tW13, CB13, x.K, x.I, 2 * x.E, x.K, skinny::ROWS) || !map_codes(&tW2, CB2, x.I, x.K, x.E, x.I, skinny::ROWS))
+      return I8_ERR_CUDA;
+    tX = tH = tW2;
+    if (!direct && (!map_codes(&tX, ws + w.xq, x.K, x.R, 0, x.K, nt) || !map_codes(&tH, ws + w.h, x.Ip, x.R, 0, x.Ip, nt)))
       return I8_ERR_CUDA;
     skinny::Args a = {};
+    a.X = X;
+    a.k_cols = x.K;
+    a.row_at = reinterpret_cast<const int32_t*>(ws + w.row_at);
+    a.copies = static_cast<int>(x.k);
     a.M = M;
     a.groups = E;
     a.offsets = offsets;
@@ -510,14 +548,19 @@ i8_status experts_forward(const void* X, int32_t dtype, const int32_t* idx, cons
     a.ldc = 2 * x.I;
     a.parts = reinterpret_cast<float*>(ws + w.parts);
     a.arrived = arrived;
-    st = run_skinny(nt, blk::kOutF32, tW13, tX, a, token_tiles, d, s);
+    const int in = !direct ? skinny::kInCodes : dtype == I8_DTYPE_BF16 ? skinny::kInBf16 : skinny::kInF16;
+    st = run_skinny(nt, blk::kOutF32, in, tW13, tX, a, token_tiles, d, s);
     if (st != I8_OK) return st;
-    const int64_t warps = x.R * x.IB, grid = (warps + 7) / 8;
-    if (!fits_int(grid)) return I8_ERR_INVALID_ARG;
-    const cudaError_t e = launch_overlapped(moe::gated_quant_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s,
-                                            static_cast<const float*>(gu), offsets + x.E, x.R, static_cast<int>(x.I),
-                                            ws + w.h, x.Ip, SH);
-    if (!cuda_ok(e, "kernel launch") || launch_status() != I8_OK) return I8_ERR_CUDA;
+    if (!direct) {
+      const int64_t warps = x.R * x.IB, grid = (warps + 7) / 8;
+      if (!fits_int(grid)) return I8_ERR_INVALID_ARG;
+      const cudaError_t e = launch_overlapped(moe::gated_quant_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s,
+                                              static_cast<const float*>(gu), offsets + x.E, x.R, static_cast<int>(x.I),
+                                              ws + w.h, x.Ip, SH);
+      if (!cuda_ok(e, "kernel launch") || launch_status() != I8_OK) return I8_ERR_CUDA;
+    }
+    a.X = gu;
+    a.k_cols = x.I;
     a.k_blocks = x.IB;
     a.n_tiles = a.n_per_z = x.KB;
     a.z_cols = static_cast<int>(x.K);
@@ -527,7 +570,7 @@ i8_status experts_forward(const void* X, int32_t dtype, const int32_t* idx, cons
     a.C = Y2;
     a.ldc = x.K;
     a.arrived = arrived + kPartGrid;
-    st = run_skinny(nt, blk::kOutF32, tW2, tH, a, token_tiles, d, s);
+    st = run_skinny(nt, blk::kOutF32, direct ? skinny::kInGated : skinny::kInCodes, tW2, tH, a, token_tiles, d, s);
   } else {
     const int64_t m_tiles = x.R / blk::TM + (x.R < x.E ? x.R : x.E);
     if (!map_codes(&tX, ws + w.xq, x.K, x.R, 0, x.K, blk::HM) || !map_codes(&tW13, CB13, x.K, x.I, 2 * x.E, x.K, 64) ||
@@ -576,7 +619,7 @@ i8_status experts_backward(const void* dY, int32_t dtype, const int32_t* idx, co
   i8_status st = block_info(d, &b);
   if (st != I8_OK) return st;
   const ExpertsWs w = experts_ws(x, true);
-  st = experts_rows(dY, dtype, idx, x, w, ws, dw, s);
+  st = experts_rows(dY, dtype, idx, x, w, ws, dw, true, s);
   if (st != I8_OK) return st;
   const int32_t* offsets = reinterpret_cast<const int32_t*>(ws + w.offsets);
   const int64_t m_tiles = x.R / blk::TM + (x.R < x.E ? x.R : x.E);

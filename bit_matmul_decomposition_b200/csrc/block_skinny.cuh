@@ -18,7 +18,8 @@
 // Design (sm_100a): one CTA an SM; warp 0 fills a ring of [128 x 128 weight | NT x 128 token]
 // stages by TMA, warp 1 issues tcgen05.mma (cta_group::1, kind::f8f6f4, M = 128, N = NT), one
 // block to one of NBUF small TMEM accumulators, warps 2..5 add them, scaled, to fp32 sums in
-// registers.  The weight does not depend on the kernel before (the quantiser of the tokens), so
+// registers, warp 6 holds the scales of the units ahead ready in shared memory (loaded by the
+// epilogue itself, one unit ahead, they were most of its time: 27 us for 67 MB of weight).  The weight does not depend on the kernel before (the quantiser of the tokens), so
 // with a tile order known from the start the ring fills with weights while that kernel runs.
 #pragma once
 
@@ -31,25 +32,41 @@ using blk::BK;
 using blk::MAX_GROUPS;
 constexpr int ROWS = 128;                    // weight rows of a tile
 constexpr int W_BYTES = ROWS * BK;
-constexpr int THREADS = 192;
+constexpr int X_WARPS = 4;                   // warps that form the tokens' codes (direct input)
+__host__ __device__ constexpr int threads(int in) { return in == 0 ? 224 : (6 + X_WARPS) * 32; }
 constexpr int PRE_BYTES = blk::PRE_BYTES;
-constexpr int BAR_BYTES = 512;
+constexpr int BAR_BYTES = 1024;
 constexpr int MAX_STAGES = 12;
 constexpr int NBUF = 4;                      // TMEM accumulators
-constexpr int RING_BUDGET = 212 * 1024;
+constexpr int RING_BUDGET = 210 * 1024;
 
 __host__ __device__ constexpr int stage_bytes(int nt) { return W_BYTES + nt * BK; }
 __host__ __device__ constexpr int stages(int nt) {
   return RING_BUDGET / stage_bytes(nt) < MAX_STAGES ? RING_BUDGET / stage_bytes(nt) : MAX_STAGES;
 }
-__host__ __device__ constexpr int scale_bytes(int nt) { return 4 * 2 * nt * 4; }
+constexpr int SLOTS = 16;                    // units whose scales are held ready
+__host__ __device__ constexpr int scale_bytes(int nt) { return SLOTS * nt * 4; }
 __host__ __device__ constexpr size_t smem_bytes(int nt) {
   return static_cast<size_t>(stages(nt)) * stage_bytes(nt) + scale_bytes(nt) + PRE_BYTES + BAR_BYTES + 1024;
 }
 static_assert(smem_bytes(16) <= 232448 && smem_bytes(32) <= 232448 && smem_bytes(64) <= 232448 &&
               smem_bytes(128) <= 232448, "shared memory per CTA");
 
+// Where the tokens' codes come from: the quantiser's, by TMA; or, for tiles of 16 tokens, formed in
+// the kernel by four warps that take the units in turn and write codes and scales straight into
+// the stage (128-byte swizzle): from the 16-bit rows of X, or from g and u as h = silu(g) * u.
+// Every CTA forms the codes of its own units again, a few hundred instructions beside a weight
+// tile that takes about 600 cycles to arrive, and the kernel that would have formed them once
+// falls away: 5.5 us and its launch.
+enum { kInCodes = 0, kInF16 = 1, kInBf16 = 2, kInGated = 3 };
+
 struct Args {
+  // direct input: rows [tokens][k_cols] of X, 16-bit, or GU [M][2][k_cols] fp32.  With groups, row
+  // p of X is the token row_at[p] / copies; GU's rows are in order.
+  const void* X;
+  int64_t k_cols;
+  const int32_t* row_at;
+  int copies;
   int M;                        // rows (tokens) in all groups
   int k_blocks;
   int n_tiles, n_per_z;         // weight tiles of a group; of one z slice of it
@@ -72,6 +89,8 @@ struct SmemBars {
   uint64_t empty[MAX_STAGES];
   uint64_t tmem_full[NBUF];
   uint64_t tmem_empty[NBUF];
+  uint64_t scaled[SLOTS];      // the unit's scales are in its slot
+  uint64_t unscaled[SLOTS];    // the epilogue is done with them
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -79,13 +98,25 @@ struct SmemBars {
 };
 static_assert(sizeof(SmemBars) <= BAR_BYTES, "barrier block");
 
-__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                          uint32_t idesc, uint32_t accumulate) {
+// as blk::umma_lead and blk::commit_lead, for one CTA
+__device__ __forceinline__ void umma_lead(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                          uint32_t accumulate, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %6};\n\t"
+      "mov.b64 db, {%2, %6};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(lead), "r"(blk::DESC_HI)
+      : "memory");
+}
+__device__ __forceinline__ void commit_lead(uint32_t bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
       : "memory");
 }
 
@@ -104,8 +135,14 @@ __device__ __forceinline__ void tmem_ld_x16_wait(uint32_t taddr, uint32_t (&r)[1
 
 __device__ __forceinline__ void epi_bar128() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-template <int NT, int kOut>
-__global__ void __launch_bounds__(THREADS, 1)
+// clears the counters of a product that no other kernel goes before
+__global__ void clear_kernel(unsigned int* zero) {
+  grid_dep_launch();
+  zero[threadIdx.x] = 0u;
+}
+
+template <int NT, int kOut, int kIn>
+__global__ void __launch_bounds__(threads(kIn), 1)
     block_skinny_kernel(const __grid_constant__ CUtensorMap tmW,
                         const __grid_constant__ CUtensorMap tmX, const Args a) {
   constexpr int STAGES = stages(NT);
@@ -119,19 +156,23 @@ __global__ void __launch_bounds__(THREADS, 1)
   float* sscale = reinterpret_cast<float*>(smem + static_cast<size_t>(STAGES) * SBYTES);
   int* pre = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(sscale) + scale_bytes(NT));
   SmemBars* bars = reinterpret_cast<SmemBars*>(reinterpret_cast<uint8_t*>(pre) + PRE_BYTES);
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // uniform in the warp
   const int lane = threadIdx.x & 31;
   volatile int* abort_flag = &bars->abort_flag;
   const uint64_t lim = a.wait_limit_ns;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(smem_u32(&bars->full[s]), 1);
+      mbar_init(smem_u32(&bars->full[s]), kIn == kInCodes ? 1 : 2);   // TMA, and the unit's x warp
       mbar_init(smem_u32(&bars->empty[s]), 1);
     }
     for (int b = 0; b < NBUF; ++b) {
       mbar_init(smem_u32(&bars->tmem_full[b]), 1);
       mbar_init(smem_u32(&bars->tmem_empty[b]), 4);
+    }
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(smem_u32(&bars->scaled[i]), 1);
+      mbar_init(smem_u32(&bars->unscaled[i]), 4);
     }
     mbar_init(smem_u32(&bars->drain), 1);
     bars->abort_flag = 0;
@@ -139,7 +180,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmW);
-    tma_prefetch_desc(&tmX);
+    if (kIn == kInCodes) tma_prefetch_desc(&tmX);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&bars->tmem_base), TMEM_COLS);
@@ -179,10 +220,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = bars->tmem_base;
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
 
   const int KB = a.k_blocks;
-  const int64_t units = static_cast<int64_t>(pre[a.groups]) * a.n_tiles * KB;
+  const int64_t units = static_cast<int64_t>(__shfl_sync(0xffffffffu, pre[a.groups], 0)) * a.n_tiles * KB;
   // G CTAs share the units, each at least one: with fewer units than CTAs (known only here, by
   // the groups' sizes) the CTAs past the last unit have none and take no part in any tile
   const int64_t G = units < static_cast<int64_t>(gridDim.x) ? units : static_cast<int64_t>(gridDim.x);
@@ -217,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // One pass over the run.  While the kernel before may still write the tokens' codes
       // (dense form), the first STAGES units get their weight half only; then the wait, their
       // token halves, and the rest of the run whole.
-      const int64_t head = grouped ? 0 : (u1 - u0 < STAGES ? u1 - u0 : STAGES);
+      const int64_t head = grouped || kIn != kInCodes ? 0 : (u1 - u0 < STAGES ? u1 - u0 : STAGES);
       auto issue = [&](int64_t u, int s, bool w, bool x, int& row0, int& z, int& nz, int& last_tile) {
         const int tile = static_cast<int>(u / KB);
         const int kb = static_cast<int>(u - static_cast<int64_t>(tile) * KB);
@@ -229,15 +270,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t dst = ring + s * SBYTES;
         const uint32_t fb = smem_u32(&bars->full[s]);
         if (w) {
-          mbar_arrive_expect_tx(fb, SBYTES);
+          mbar_arrive_expect_tx(fb, kIn == kInCodes ? SBYTES : W_BYTES);
           tma_load_3d(dst, &tmW, fb, kb * BK, nz * ROWS, z);
         }
-        if (x) tma_load_2d(dst + W_BYTES, &tmX, fb, kb * BK, row0);
+        if (x && kIn == kInCodes) tma_load_2d(dst + W_BYTES, &tmX, fb, kb * BK, row0);
       };
       int row0 = 0, z = 0, nz = 0, last_tile = -1;
       for (int64_t i = 0; i < head; ++i) issue(u0 + i, static_cast<int>(i), true, false, row0, z, nz, last_tile);
       if (!grouped) {
-        grid_dep_wait();
+        if (kIn == kInCodes) grid_dep_wait();
         grid_dep_launch();
       }
       last_tile = -1;
@@ -268,40 +309,177 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------------------------------------------------------- MMA issuer
-      constexpr uint32_t ID = idesc_e4m3_f32(ROWS, NT);
-      int s = 0;
-      uint32_t ph = 0, n = 0;
-      for (int64_t u = u0; u < u1; ++u, ++n) {
-        const uint32_t b = n % NBUF;
-        if (!mbar_wait(smem_u32(&bars->tmem_empty[b]), ((n / NBUF) & 1u) ^ 1u, abort_flag, lim) ||
-            !mbar_wait(smem_u32(&bars->full[s]), ph, abort_flag, lim))
-          break;
-        tc_fence_after();
-        const uint32_t sw = ring + s * SBYTES;
+    // ------------------------------------------------------------------ MMA issuer
+    // the whole warp walks the loop (uniform descriptors), lane 0 issues
+    constexpr uint32_t ID = idesc_e4m3_f32(ROWS, NT);
+    const uint32_t lead = lane == 0 ? 1u : 0u;
+    const uint32_t w0 = blk::desc_lo<false>(ring), x0 = blk::desc_lo<false>(ring + W_BYTES);
+    int s = 0;
+    uint32_t ph = 0, n = 0;
+    for (int64_t u = u0; u < u1; ++u, ++n) {
+      const uint32_t b = n % NBUF;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->tmem_empty[b]), ((n / NBUF) & 1u) ^ 1u, abort_flag, lim) &&
+                                       mbar_wait(smem_u32(&bars->full[s]), ph, abort_flag, lim)))
+        break;
+      tc_fence_after();
+      const uint32_t so = static_cast<uint32_t>(s) * (SBYTES >> 4);
 #pragma unroll
-        for (int kk = 0; kk < BK / 32; ++kk)
-          umma_e4m3(tmem_base + b * NT, sdesc_k_sw128(sw + kk * 32), sdesc_k_sw128(sw + W_BYTES + kk * 32), ID, kk != 0);
-        umma_commit(smem_u32(&bars->empty[s]));
-        umma_commit(smem_u32(&bars->tmem_full[b]));
-        if (++s == STAGES) {
-          s = 0;
-          ph ^= 1u;
+      for (int kk = 0; kk < BK / 32; ++kk)
+        umma_lead(tmem_base + b * NT, w0 + so + kk * 2, x0 + so + kk * 2, ID, kk != 0, lead);
+      commit_lead(smem_u32(&bars->empty[s]), lead);
+      commit_lead(smem_u32(&bars->tmem_full[b]), lead);
+      if (++s == STAGES) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+    int no_abort = 0;
+    commit_lead(smem_u32(&bars->drain), lead);
+    mbar_wait(smem_u32(&bars->drain), 0u, &no_abort, lim);
+  } else if (warp >= 6 && kIn != kInCodes) {
+    // ------------------------------------------------------------------ token codes
+    // Unit i of the run belongs to warp 6 + i % X_WARPS.  Lane l holds half (l & 1) of the block of
+    // token l / 2: 64 features.  Rows past the tile's tokens keep what the stage held: their
+    // columns of the product are never read.
+    const int xw = warp - 6;
+    const int r = lane >> 1, hf = lane & 1;
+    int tile = -1, row0 = 0, row_end = 0, z = 0, nz = 0;
+    uint32_t n = static_cast<uint32_t>(xw);
+    for (int64_t u = u0 + xw; u < u1; u += X_WARPS, n += X_WARPS) {
+      const int t = static_cast<int>(u / KB);
+      const int kb = static_cast<int>(u - static_cast<int64_t>(t) * KB);
+      if (t != tile) {
+        tile_at(t, row0, row_end, z, nz);
+        tile = t;
+      }
+      const float w = __ldg(a.SB + (static_cast<int64_t>(z) * a.n_per_z + nz) * KB + kb);
+      const int64_t col = static_cast<int64_t>(kb) * BK + hf * 64;
+      const bool live = row0 + r < row_end;
+      uint4 raw[8];                                 // X: 64 values
+      float h[64];                                  // GU
+      float am = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (kIn == kInGated) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) h[i] = 0.0f;
+        if (live) {
+          const float* g = static_cast<const float*>(a.X) + static_cast<int64_t>(row0 + r) * 2 * a.k_cols + col;
+#pragma unroll
+          for (int i = 0; i < 64; i += 4)
+            if (col + i < a.k_cols) {
+              const float4 gv = __ldg(reinterpret_cast<const float4*>(g + i));
+              const float4 uv = __ldg(reinterpret_cast<const float4*>(g + a.k_cols + i));
+              h[i] = gv.x * blk::fast_sigmoid(gv.x) * uv.x;
+              h[i + 1] = gv.y * blk::fast_sigmoid(gv.y) * uv.y;
+              h[i + 2] = gv.z * blk::fast_sigmoid(gv.z) * uv.z;
+              h[i + 3] = gv.w * blk::fast_sigmoid(gv.w) * uv.w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 64; ++i) am = fmaxf(am, fabsf(h[i]));
+      } else {
+        if (live) {
+          const int64_t token = a.row_at != nullptr ? __ldg(a.row_at + row0 + r) / a.copies : row0 + r;
+          const uint16_t* x = static_cast<const uint16_t*>(a.X) + token * a.k_cols + col;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (col + 8 * i < a.k_cols) raw[i] = ldg_v4(x + 8 * i);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float f[8];
+          blk::unpack8<kIn == kInBf16>(raw[i], f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) am = fmaxf(am, fabsf(f[j]));
         }
       }
-      int no_abort = 0;
-      umma_commit(smem_u32(&bars->drain));
-      mbar_wait(smem_u32(&bars->drain), 0u, &no_abort, lim);
+      am = fmaxf(fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1)), blk::kScaleFloor);
+      const float up = blk::block_up(am);
+      const int s = static_cast<int>(n % STAGES);
+      // the stage is free, and with it the slot: its last unit's MMAs are done, so TMEM was free for
+      // them, so the epilogue is past unit n - STAGES - NBUF >= n - SLOTS
+      static_assert(SLOTS >= STAGES + NBUF, "slot reuse");
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->empty[s]), ((n / STAGES) & 1u) ^ 1u, abort_flag, lim))) break;
+      if (live) {
+        const uint32_t base = ring + s * SBYTES + W_BYTES + static_cast<uint32_t>(r * 128);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {               // 16 codes at a time
+          float f[16];
+          if (kIn == kInGated) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f[j] = h[16 * i + j];
+          } else {
+            float lo[8], hi[8];
+            blk::unpack8<kIn == kInBf16>(raw[2 * i], lo);
+            blk::unpack8<kIn == kInBf16>(raw[2 * i + 1], hi);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              f[j] = lo[j];
+              f[8 + j] = hi[j];
+            }
+          }
+          const float f0[8] = {f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7]};
+          const float f1[8] = {f[8], f[9], f[10], f[11], f[12], f[13], f[14], f[15]};
+          const uint2 x = blk::codes8_scaled(f0, up), y = blk::codes8_scaled(f1, up);
+          const uint32_t chunk = static_cast<uint32_t>((hf * 4 + i) ^ (r & 7));
+          gemm::sts_v4(base + chunk * 16u, x.x, x.y, y.x, y.y);
+        }
+        if (hf == 0) sscale[(n % SLOTS) * NT + r] = blk::block_down(am) * w;
+      }
+      gemm::fence_proxy_async_smem();               // the tensor cores read what these lanes wrote
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&bars->scaled[n % SLOTS]));
+        mbar_arrive(smem_u32(&bars->full[s]));
+      }
+    }
+  } else if (warp == 6) {
+    // ------------------------------------------------------------------ scales
+    // SA * SB of each unit's tokens, AHEAD units loaded together
+    if (!grouped) grid_dep_wait();
+    constexpr int SL = (NT + 31) / 32;              // tokens of a lane
+    constexpr int AHEAD = SL > 2 ? 4 : 8;
+    uint32_t n = 0;
+    int tile = -1, row0 = 0, row_end = 0, z = 0, nz = 0;
+    bool ok = true;
+    for (int64_t u = u0; u < u1 && ok; u += AHEAD) {
+      float v[AHEAD][SL], w[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        if (u + i >= u1) break;
+        const int t = static_cast<int>((u + i) / KB);
+        const int kb = static_cast<int>(u + i - static_cast<int64_t>(t) * KB);
+        if (t != tile) {
+          tile_at(t, row0, row_end, z, nz);
+          tile = t;
+        }
+        w[i] = __ldg(a.SB + (static_cast<int64_t>(z) * a.n_per_z + nz) * KB + kb);
+#pragma unroll
+        for (int l = 0; l < SL; ++l) {
+          const int r = row0 + lane + 32 * l;
+          v[i][l] = __ldg(a.SA + static_cast<int64_t>(kb) * a.M + (r < a.M ? r : a.M - 1));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        if (u + i >= u1) break;
+        const uint32_t slot = n % SLOTS;
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->unscaled[slot]), ((n / SLOTS) & 1u) ^ 1u, abort_flag, lim));
+        if (!ok) break;
+#pragma unroll
+        for (int l = 0; l < SL; ++l)
+          if (lane + 32 * l < NT) sscale[slot * NT + lane + 32 * l] = v[i][l] * w[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->scaled[slot]));
+        ++n;
+      }
     }
   } else {
     // ------------------------------------------------------------------ epilogue
-    if (!grouped) grid_dep_wait();
     const int q = warp & 3;
     const int nl = q * 32 + lane;                   // the thread's weight row in the tile
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-    float* sc = sscale + q * 2 * NT;                // this warp's two rows of scales
-    constexpr int SL = (NT + 31) / 32;              // scales a lane loads
     uint32_t n = 0;
     bool dead = false;
     for (int64_t u = u0; u < u1;) {
@@ -311,29 +489,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int kb1 = static_cast<int>((t0 + KB < u1 ? t0 + KB : u1) - t0);
       int row0, row_end, z, nz;
       tile_at(tile, row0, row_end, z, nz);
-      const float* sb = a.SB + (static_cast<int64_t>(z) * a.n_per_z + nz) * KB;
       float acc[NT];
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[j] = 0.0f;
-      float nx[SL];
-      auto load_scales = [&](int kb) {
-        const float w = __ldg(sb + kb);
-#pragma unroll
-        for (int i = 0; i < SL; ++i) {
-          const int t = row0 + lane + 32 * i;
-          nx[i] = __ldg(a.SA + static_cast<int64_t>(kb) * a.M + (t < a.M ? t : a.M - 1)) * w;
-        }
-      };
-      if (!dead) load_scales(kb0);
       for (int kb = kb0; kb < kb1 && !dead; ++kb, ++n) {
         const uint32_t b = n % NBUF;
-        float* row = sc + (n & 1u) * NT;
-#pragma unroll
-        for (int i = 0; i < SL; ++i)
-          if (lane + 32 * i < NT) row[lane + 32 * i] = nx[i];
-        __syncwarp();
-        if (kb + 1 < kb1) load_scales(kb + 1);
-        const bool got = mbar_wait(smem_u32(&bars->tmem_full[b]), (n / NBUF) & 1u, abort_flag, lim);
+        const float* row = sscale + (n % SLOTS) * NT;
+        const bool got = mbar_wait(smem_u32(&bars->scaled[n % SLOTS]), (n / SLOTS) & 1u, abort_flag, lim) &&
+                         mbar_wait(smem_u32(&bars->tmem_full[b]), (n / NBUF) & 1u, abort_flag, lim);
         if (!__all_sync(0xffffffffu, got)) {
           dead = true;
           break;
@@ -354,11 +517,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->tmem_empty[b]));
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bars->tmem_empty[b]));
+          if (kIn == kInCodes) mbar_arrive(smem_u32(&bars->unscaled[n % SLOTS]));
+        }
       }
       u = t0 + kb1;
       bool write = !dead;
       if (kb0 != 0 || kb1 != KB) {
+        if (!grouped) grid_dep_wait();              // the counters are cleared by the kernel before
         // the CTAs that share this tile, and this one's part of it
         const int64_t me = blockIdx.x;
         int64_t c0 = t0 * G / units, c1 = (t0 + KB - 1) * G / units;   // estimates, then exact
@@ -370,7 +537,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         float* part = a.parts + slot(me) * (NT * ROWS) + nl;
         if (!dead) {
 #pragma unroll
-          for (int j = 0; j < NT; ++j) part[j * ROWS] = acc[j];
+          for (int j = 0; j < NT; ++j)
+            if (row0 + j < row_end) part[j * ROWS] = acc[j];
         }
         __threadfence();
         epi_bar128();
@@ -385,7 +553,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int64_t c = c0; c <= c1; ++c) {
             const float* p = a.parts + slot(c) * (NT * ROWS) + nl;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) acc[j] += __ldcg(p + j * ROWS);
+            for (int j = 0; j < NT; ++j)
+              if (row0 + j < row_end) acc[j] += __ldcg(p + j * ROWS);
           }
         }
       }
@@ -411,6 +580,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   }
 
+  grid_dep_wait();                                  // no CTA ends before the kernel before it
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -274,17 +274,20 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 // own, then numbers its own in order: offsets[e], place[r] (the row's position, -1 without an
 // expert) and row_at[position].  Positions are a stable sort by expert: no atomics, so the same
 // on every run.  An index outside [0, E) that is not negative sets the error word and counts as
-// none.  With `dw`, the entries of rows without an expert are cleared.
+// none.  With `dw`, the entries of rows without an expert are cleared; CTA 0 clears `zero`, the
+// counters of the products that follow.
 constexpr int kSortThreads = 512;
 
 __global__ void __launch_bounds__(kSortThreads)
     sort_rows_kernel(const int32_t* __restrict__ idx, int64_t R, int E, int32_t* __restrict__ offsets,
                      int32_t* __restrict__ place, int32_t* __restrict__ row_at,
-                     float* __restrict__ dw) {
+                     float* __restrict__ dw, unsigned int* __restrict__ zero, int zero_words) {
   __shared__ int s_less[kSortThreads / 32], s_eq[kSortThreads / 32];
   const int e = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = lane_id();
   grid_dep_launch();
+  if (e == 0)
+    for (int i = threadIdx.x; i < zero_words; i += kSortThreads) zero[i] = 0u;
   int less = 0, eq = 0;
   for (int64_t r = threadIdx.x; r < R; r += kSortThreads) {
     const int v = __ldg(idx + r);

@@ -14,35 +14,38 @@ from __future__ import annotations
 from typing import Iterable, Optional, Tuple
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import abi
-from .block import DTYPES, _check_input, _dense, quantize_weight_blocks
+from .block import DTYPES, _check_input, _dense, _on, quantize_weight_blocks
+
+
+def _route(logits, balance, score, n_groups, top_groups, k, renormalize, scale):
+    T = logits.shape[0]
+    w = logits.new_empty((T, k), dtype=torch.float32)
+    idx = logits.new_empty((T, k), dtype=torch.int32)
+    if T > 0:
+        with _on(logits.device):
+            abi.i8_route_experts(logits, balance, score, n_groups, top_groups, k, renormalize,
+                                 scale, w, idx)
+    return w, idx
 
 
 class _RouteFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, balance, score, n_groups, top_groups, k, renormalize, scale):
-        T = logits.shape[0]
-        w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-        idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-        if T > 0:
-            with torch.cuda.device(logits.device):
-                abi.i8_route_experts(logits, balance, score, n_groups, top_groups, k,
-                                     renormalize, scale, w, idx)
+        w, idx = _route(logits, balance, score, n_groups, top_groups, k, renormalize, scale)
         ctx.save_for_backward(logits, idx)
         ctx.how = (score, renormalize, scale)
         ctx.mark_non_differentiable(idx)
         return w, idx
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, gw, _):
         logits, idx = ctx.saved_tensors
         gl = torch.empty_like(logits)
         if logits.shape[0] > 0:
-            with torch.cuda.device(logits.device):
-                abi.i8_route_experts_backward(logits, *ctx.how, idx, _dense(gw.float()), gl)
+            with _on(logits.device):
+                abi.i8_route_experts_backward(logits, *ctx.how, idx, _dense(gw), gl)
         return (gl,) + (None,) * 7
 
 
@@ -75,8 +78,14 @@ def route_experts(logits: torch.Tensor, top_k: int, balance: Optional[torch.Tens
             raise ValueError("balance on %s, logits on %s" % (balance.device, logits.device))
         balance = _dense(balance.detach())
     lead = logits.shape[:-1]
-    w, idx = _RouteFn.apply(_dense(logits.reshape(-1, E)), balance, score, int(n_groups),
-                            int(top_groups), int(top_k), bool(renormalize), float(scale))
+    x = logits if len(lead) == 1 else logits.reshape(-1, E)
+    how = (_dense(x), balance, score, n_groups, top_groups, top_k, renormalize, scale)
+    if logits.requires_grad and torch.is_grad_enabled():
+        w, idx = _RouteFn.apply(*how)
+    else:
+        w, idx = _route(*how)
+    if len(lead) == 1:
+        return w, idx
     return w.view(*lead, top_k), idx.view(*lead, top_k)
 
 
@@ -84,12 +93,11 @@ def _forward(x2, idx, w, CB13, S13, CB2, S2, keep):
     T, K = x2.shape
     E, _, I, _ = CB13.shape
     k = idx.shape[1]
-    y = torch.empty((T, K), dtype=x2.dtype, device=x2.device)
-    gu = torch.empty((T * k, 2, I), dtype=torch.float32, device=x2.device) if keep else None
+    y = x2.new_empty((T, K))
+    gu = w.new_empty((T * k, 2, I)) if keep else None
     if T > 0:
-        ws = torch.empty((abi.i8_experts_workspace_size(T, K, I, E, k),), dtype=torch.uint8,
-                         device=x2.device)
-        with torch.cuda.device(x2.device):
+        ws = CB13.new_empty(abi.i8_experts_workspace_size(T, K, I, E, k), dtype=torch.uint8)
+        with _on(x2.device):
             abi.i8_experts_forward(x2, idx, w, CB13, S13, CB2, S2, y, gu, ws)
     return y, gu
 
@@ -103,17 +111,16 @@ class _ExpertsFn(torch.autograd.Function):
         return y
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, gy):
         w, idx, CB13, S13, CB2, S2, gu = ctx.saved_tensors
-        gy = _dense(gy.to(ctx.dtype))
+        gy = _dense(gy if gy.dtype == ctx.dtype else gy.to(ctx.dtype))
         (T, K), k = gy.shape, idx.shape[1]
         E, _, I, _ = CB13.shape
         gx, gw = torch.empty_like(gy), torch.empty_like(w)
         if T > 0:
-            ws = torch.empty((abi.i8_experts_backward_workspace_size(T, K, I, E, k),),
-                             dtype=torch.uint8, device=gy.device)
-            with torch.cuda.device(gy.device):
+            ws = CB13.new_empty(abi.i8_experts_backward_workspace_size(T, K, I, E, k),
+                                dtype=torch.uint8)
+            with _on(gy.device):
                 abi.i8_experts_backward(gy, idx, w, CB13, S13, CB2, S2, gu, gx, gw, ws)
         return gx, gw, None, None, None, None, None
 
@@ -144,12 +151,12 @@ def experts_block_fp8(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor,
     k = idx.shape[-1]
     if CB13.shape[0] > 512 or not 1 <= k <= 32:
         raise ValueError("%d experts, %d a token: at most 512 and 1 to 32" % (CB13.shape[0], k))
-    x2, i2, w2 = _dense(x.reshape(-1, K)), _dense(idx.reshape(-1, k)), _dense(weights.reshape(-1, k))
+    x2, i2, w2 = (_dense(t if t.dim() == 2 else t.reshape(-1, t.shape[-1])) for t in (x, idx, weights))
     if torch.is_grad_enabled() and (x2.requires_grad or w2.requires_grad):
         y = _ExpertsFn.apply(x2, w2, i2, CB13, S13, CB2, S2)
     else:
         y, _ = _forward(x2, i2, w2, CB13, S13, CB2, S2, False)
-    return y.view(x.shape)
+    return y if x.dim() == 2 else y.view(x.shape)
 
 
 class ExpertsBlockFp8(torch.nn.Module):

@@ -137,16 +137,19 @@ bool map_codes(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int
 
 // ------------------------------------------------------------------ stage launchers
 // after: launched with programmatic serialization (its kernel waits for the one before)
-i8_status run_block_quant(int32_t dtype, const blk::QuantArgs& a, int64_t Z, bool after, cudaStream_t s) {
+i8_status run_block_quant(int32_t dtype, blk::QuantArgs a, int64_t Z, bool after, cudaStream_t s) {
+  const bool rows = a.Qr != nullptr, tiles = a.Qt != nullptr, bf = dtype == I8_DTYPE_BF16;
+  const bool thin = rows && !tiles && a.colsum == nullptr;    // row codes alone: 32 rows a CTA
+  if (thin) a.row_blocks = static_cast<int>((a.R + 31) / 32);
   const int64_t grid = Z * a.row_blocks * a.col_blocks;
   if (!fits_int(grid)) return I8_ERR_INVALID_ARG;
-  const bool rows = a.Qr != nullptr, tiles = a.Qt != nullptr, bf = dtype == I8_DTYPE_BF16;
   using Fn = void (*)(blk::QuantArgs);
-  const Fn fns[8] = {blk::block_quant_kernel<false, false, false>, blk::block_quant_kernel<false, false, true>,
-                     blk::block_quant_kernel<false, true, false>, blk::block_quant_kernel<false, true, true>,
-                     blk::block_quant_kernel<true, false, false>, blk::block_quant_kernel<true, false, true>,
-                     blk::block_quant_kernel<true, true, false>, blk::block_quant_kernel<true, true, true>};
-  const Fn f = fns[(bf ? 4 : 0) + (rows ? 2 : 0) + (tiles ? 1 : 0)];
+  const Fn fns[10] = {blk::block_quant_kernel<false, false, false, 8>, blk::block_quant_kernel<false, false, true, 8>,
+                      blk::block_quant_kernel<false, true, false, 8>, blk::block_quant_kernel<false, true, true, 8>,
+                      blk::block_quant_kernel<true, false, false, 8>, blk::block_quant_kernel<true, false, true, 8>,
+                      blk::block_quant_kernel<true, true, false, 8>, blk::block_quant_kernel<true, true, true, 8>,
+                      blk::block_quant_kernel<false, true, false, 2>, blk::block_quant_kernel<true, true, false, 2>};
+  const Fn f = fns[thin ? 8 + (bf ? 1 : 0) : (bf ? 4 : 0) + (rows ? 2 : 0) + (tiles ? 1 : 0)];
   if (after) {
     const cudaError_t e = launch_overlapped(f, dim3(static_cast<unsigned>(grid)), dim3(blk::kQuantThreads), 0, s, a);
     return cuda_ok(e, "kernel launch") ? launch_status() : I8_ERR_CUDA;

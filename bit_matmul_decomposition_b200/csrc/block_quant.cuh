@@ -12,7 +12,7 @@
 // tile), and no other.
 //
 // One CTA of 256 threads holds a 128 x 128 tile of the input in registers (eight 16-byte
-// groups a thread, all in flight at once), so one read of the input gives any of: its row
+// groups a thread, all in flight at once; 32 rows where only row codes are wanted), so one read of the input gives any of: its row
 // codes, its tile codes, its column sums.  The pass is bound by HBM: 2 bytes read and 1 written
 // per value and code set.
 #pragma once
@@ -54,6 +54,20 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// largest |v| of 8 packed values (two at a time; a NaN gives way to the other operand)
+template <bool kBf16>
+__device__ __forceinline__ float absmax8(const uint4& v) {
+  const uint32_t w[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
+  if (kBf16) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(w);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+  const __half2* h = reinterpret_cast<const __half2*>(w);
+  const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+  return fmaxf(__low2float(m), __high2float(m));
 }
 
 struct QuantArgs {
@@ -98,9 +112,12 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   }
 }
 
-template <bool kBf16, bool kRows, bool kTiles>
-__global__ void __launch_bounds__(kQuantThreads)
+// PASSES: rows of 16 a thread holds; 8 for tiles, 2 when row codes alone are wanted (four times the
+// CTAs: 2048 x 4096 took X us with 128 rows a CTA, Y us with 32).
+template <bool kBf16, bool kRows, bool kTiles, int PASSES>
+__global__ void __launch_bounds__(kQuantThreads, PASSES == 2 ? 6 : kRows && kTiles ? 3 : 4)
     block_quant_kernel(const QuantArgs a) {
+  static_assert(PASSES == 8 || !kTiles, "a tile has 128 rows");
   __shared__ float s_max[kQuantThreads / 32];
   __shared__ float s_sum[16][QB];
   grid_dep_wait();
@@ -114,12 +131,12 @@ __global__ void __launch_bounds__(kQuantThreads)
   const int64_t z = b / a.row_blocks;
   const int r_in = threadIdx.x >> 4;                 // 16 rows a pass, 16 threads a row
   const int64_t c0 = static_cast<int64_t>(cb) * QB + (threadIdx.x & 15) * 8;
-  const int64_t row0 = static_cast<int64_t>(rb) * QB + r_in;
+  const int64_t row0 = static_cast<int64_t>(rb) * (PASSES * 16) + r_in;
   const uint16_t* X = a.X + z * a.R * a.C;
   const bool vec = (a.C & 7) == 0;                   // rows start on 16 bytes
-  uint4 v[8];
+  uint4 v[PASSES];
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
+  for (int p = 0; p < PASSES; ++p) {
     const int64_t r = row0 + p * 16;
     v[p] = make_uint4(0u, 0u, 0u, 0u);
     if (r < a.R) {
@@ -135,18 +152,12 @@ __global__ void __launch_bounds__(kQuantThreads)
       }
     }
   }
-  float m[8];                                        // the row's maximum over this thread's 8
+  float m[PASSES];                                        // the row's maximum over this thread's 8
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    float f[8];
-    unpack8<kBf16>(v[p], f);
-    m[p] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m[p] = fmaxf(m[p], fabsf(f[i]));
-  }
+  for (int p = 0; p < PASSES; ++p) m[p] = absmax8<kBf16>(v[p]);
   if (kRows) {
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
+    for (int p = 0; p < PASSES; ++p) {
       const int64_t r = row0 + p * 16;
       float am = m[p];
 #pragma unroll
@@ -169,7 +180,7 @@ __global__ void __launch_bounds__(kQuantThreads)
   if (kTiles) {
     float am = m[0];
 #pragma unroll
-    for (int p = 1; p < 8; ++p) am = fmaxf(am, m[p]);
+    for (int p = 1; p < PASSES; ++p) am = fmaxf(am, m[p]);
     am = warp_max(am);
     if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = am;
     __syncthreads();
@@ -179,7 +190,7 @@ __global__ void __launch_bounds__(kQuantThreads)
     am = fmaxf(am, kScaleFloor);
     const float up = block_up(am);
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
+    for (int p = 0; p < PASSES; ++p) {
       const int64_t r = row0 + p * 16;
       if (r >= a.R || c0 >= a.qt_pitch) continue;
       float f[8];
@@ -193,7 +204,7 @@ __global__ void __launch_bounds__(kQuantThreads)
     // a column in turn
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
+    for (int p = 0; p < PASSES; ++p) {
       float f[8];
       unpack8<kBf16>(v[p], f);
 #pragma unroll

@@ -32,7 +32,7 @@ using blk::BK;
 using blk::MAX_GROUPS;
 constexpr int ROWS = 128;                    // weight rows of a tile
 constexpr int W_BYTES = ROWS * BK;
-constexpr int X_WARPS = 4;                   // warps that form the tokens' codes (direct input)
+constexpr int X_WARPS = 8;                   // warps that form the tokens' codes (direct input)
 __host__ __device__ constexpr int threads(int in) { return in == 0 ? 224 : (6 + X_WARPS) * 32; }
 constexpr int PRE_BYTES = blk::PRE_BYTES;
 constexpr int BAR_BYTES = 1024;
@@ -53,7 +53,7 @@ static_assert(smem_bytes(16) <= 232448 && smem_bytes(32) <= 232448 && smem_bytes
               smem_bytes(128) <= 232448, "shared memory per CTA");
 
 // Where the tokens' codes come from: the quantiser's, by TMA; or, for tiles of 16 tokens, formed in
-// the kernel by four warps that take the units in turn and write codes and scales straight into
+// the kernel by eight warps that take the units in turn and write codes and scales straight into
 // the stage (128-byte swizzle): from the 16-bit rows of X, or from g and u as h = silu(g) * u.
 // Every CTA forms the codes of its own units again, a few hundred instructions beside a weight
 // tile that takes about 600 cycles to arrive, and the kernel that would have formed them once
@@ -338,11 +338,11 @@ __global__ void __launch_bounds__(threads(kIn), 1)
     mbar_wait(smem_u32(&bars->drain), 0u, &no_abort, lim);
   } else if (warp >= 6 && kIn != kInCodes) {
     // ------------------------------------------------------------------ token codes
-    // Unit i of the run belongs to warp 6 + i % X_WARPS.  Lane l holds half (l & 1) of the block of
-    // token l / 2: 64 features.  Rows past the tile's tokens keep what the stage held: their
-    // columns of the product are never read.
+    // Unit i of the run belongs to warp 6 + i % X_WARPS.  Eight lanes hold a token's block, 16
+    // features each; the warp takes four tokens at a time, as many times as the tile has tokens.
+    // Rows past the tile's tokens keep what the stage held: their columns are never read.
     const int xw = warp - 6;
-    const int r = lane >> 1, hf = lane & 1;
+    const int c = lane & 7;                         // 16-byte chunk of the token's codes
     int tile = -1, row0 = 0, row_end = 0, z = 0, nz = 0;
     uint32_t n = static_cast<uint32_t>(xw);
     for (int64_t u = u0 + xw; u < u1; u += X_WARPS, n += X_WARPS) {
@@ -353,80 +353,83 @@ __global__ void __launch_bounds__(threads(kIn), 1)
         tile = t;
       }
       const float w = __ldg(a.SB + (static_cast<int64_t>(z) * a.n_per_z + nz) * KB + kb);
-      const int64_t col = static_cast<int64_t>(kb) * BK + hf * 64;
-      const bool live = row0 + r < row_end;
-      uint4 raw[8];                                 // X: 64 values
-      float h[64];                                  // GU
-      float am = 0.0f;
+      const int64_t col = static_cast<int64_t>(kb) * BK + c * 16;
+      const bool in = col < a.k_cols;               // k_cols % 16 == 0: a chunk is whole or absent
+      const int turns = (min(row_end - row0, NT) + 3) >> 2;
+      const int s = static_cast<int>(n % STAGES);
+      const uint32_t xs = ring + s * SBYTES + W_BYTES;
+      bool ok = true;
+      uint4 raw[4][2];                              // X: every turn's values, loaded together
+      if (kIn != kInGated) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (kIn == kInGated) {
-#pragma unroll
-        for (int i = 0; i < 64; ++i) h[i] = 0.0f;
-        if (live) {
-          const float* g = static_cast<const float*>(a.X) + static_cast<int64_t>(row0 + r) * 2 * a.k_cols + col;
-#pragma unroll
-          for (int i = 0; i < 64; i += 4)
-            if (col + i < a.k_cols) {
-              const float4 gv = __ldg(reinterpret_cast<const float4*>(g + i));
-              const float4 uv = __ldg(reinterpret_cast<const float4*>(g + a.k_cols + i));
-              h[i] = gv.x * blk::fast_sigmoid(gv.x) * uv.x;
-              h[i + 1] = gv.y * blk::fast_sigmoid(gv.y) * uv.y;
-              h[i + 2] = gv.z * blk::fast_sigmoid(gv.z) * uv.z;
-              h[i + 3] = gv.w * blk::fast_sigmoid(gv.w) * uv.w;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 64; ++i) am = fmaxf(am, fabsf(h[i]));
-      } else {
-        if (live) {
-          const int64_t token = a.row_at != nullptr ? __ldg(a.row_at + row0 + r) / a.copies : row0 + r;
-          const uint16_t* x = static_cast<const uint16_t*>(a.X) + token * a.k_cols + col;
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (col + 8 * i < a.k_cols) raw[i] = ldg_v4(x + 8 * i);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float f[8];
-          blk::unpack8<kIn == kInBf16>(raw[i], f);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) am = fmaxf(am, fabsf(f[j]));
+        for (int i = 0; i < 4; ++i) {
+          const int p = row0 + i * 4 + (lane >> 3);
+          if (i < turns && p < row_end && in) {
+            const int64_t token = a.row_at != nullptr ? __ldg(a.row_at + p) / a.copies : p;
+            const uint16_t* x = static_cast<const uint16_t*>(a.X) + token * a.k_cols + col;
+            raw[i][0] = ldg_v4(x);
+            raw[i][1] = ldg_v4(x + 8);
+          }
         }
       }
-      am = fmaxf(fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1)), blk::kScaleFloor);
-      const float up = blk::block_up(am);
-      const int s = static_cast<int>(n % STAGES);
-      // the stage is free, and with it the slot: its last unit's MMAs are done, so TMEM was free for
-      // them, so the epilogue is past unit n - STAGES - NBUF >= n - SLOTS
-      static_assert(SLOTS >= STAGES + NBUF, "slot reuse");
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->empty[s]), ((n / STAGES) & 1u) ^ 1u, abort_flag, lim))) break;
-      if (live) {
-        const uint32_t base = ring + s * SBYTES + W_BYTES + static_cast<uint32_t>(r * 128);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {               // 16 codes at a time
-          float f[16];
+      for (int i = 0; i < 4; ++i) {
+        if (i >= turns) break;
+        const int r = i * 4 + (lane >> 3);
+        const bool live = row0 + r < row_end;
+        float f[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) f[j] = 0.0f;
+        if (live && in) {
           if (kIn == kInGated) {
+            const float* g = static_cast<const float*>(a.X) + static_cast<int64_t>(row0 + r) * 2 * a.k_cols + col;
+            float4 gv[4], uv[4];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] = h[16 * i + j];
+            for (int j = 0; j < 4; ++j) {
+              gv[j] = __ldg(reinterpret_cast<const float4*>(g) + j);
+              uv[j] = __ldg(reinterpret_cast<const float4*>(g + a.k_cols) + j);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              f[4 * j] = gv[j].x * blk::fast_sigmoid(gv[j].x) * uv[j].x;
+              f[4 * j + 1] = gv[j].y * blk::fast_sigmoid(gv[j].y) * uv[j].y;
+              f[4 * j + 2] = gv[j].z * blk::fast_sigmoid(gv[j].z) * uv[j].z;
+              f[4 * j + 3] = gv[j].w * blk::fast_sigmoid(gv[j].w) * uv[j].w;
+            }
           } else {
             float lo[8], hi[8];
-            blk::unpack8<kIn == kInBf16>(raw[2 * i], lo);
-            blk::unpack8<kIn == kInBf16>(raw[2 * i + 1], hi);
+            blk::unpack8<kIn == kInBf16>(raw[i][0], lo);
+            blk::unpack8<kIn == kInBf16>(raw[i][1], hi);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               f[j] = lo[j];
               f[8 + j] = hi[j];
             }
           }
+        }
+        float am = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) am = fmaxf(am, fabsf(f[j]));
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+        am = fmaxf(am, blk::kScaleFloor);
+        const float up = blk::block_up(am);
+        if (i == 0) {
+          // the stage is free, and with it the slot: its last unit's MMAs are done, so TMEM was free
+          // for them, so the epilogue is past unit n - STAGES - NBUF >= n - SLOTS
+          static_assert(kIn == kInCodes || SLOTS >= STAGES + NBUF, "slot reuse");
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->empty[s]), ((n / STAGES) & 1u) ^ 1u, abort_flag, lim));
+          if (!ok) break;
+        }
+        if (live) {
           const float f0[8] = {f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7]};
           const float f1[8] = {f[8], f[9], f[10], f[11], f[12], f[13], f[14], f[15]};
           const uint2 x = blk::codes8_scaled(f0, up), y = blk::codes8_scaled(f1, up);
-          const uint32_t chunk = static_cast<uint32_t>((hf * 4 + i) ^ (r & 7));
-          gemm::sts_v4(base + chunk * 16u, x.x, x.y, y.x, y.y);
+          gemm::sts_v4(xs + static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)), x.x, x.y, y.x, y.y);
+          if (c == 0) sscale[(n % SLOTS) * NT + r] = blk::block_down(am) * w;
         }
-        if (hf == 0) sscale[(n % SLOTS) * NT + r] = blk::block_down(am) * w;
       }
+      if (!ok) break;
       gemm::fence_proxy_async_smem();               // the tensor cores read what these lanes wrote
       __syncwarp();
       if (lane == 0) {

@@ -97,49 +97,69 @@ __device__ __forceinline__ bool route_scores(const RouteArgs& a, int64_t t, floa
   return !__any_sync(0xffffffffu, bad);
 }
 
-__device__ __forceinline__ double neg_inf_d() { return __longlong_as_double(0xfff0000000000000ll); }
+// An fp64 key as an unsigned number of the same order (0 below all of them: no live expert).
+__device__ __forceinline__ uint64_t ordered(double v) {
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));   // -0 as +0
+  return (b >> 63) ? ~b : b | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double unordered(uint64_t k) {
+  return __longlong_as_double(static_cast<long long>((k >> 63) ? k & 0x7fffffffffffffffull : ~k));
+}
 
-// the largest (key, lowest index) of the warp
-__device__ __forceinline__ void warp_best(double& key, int& e) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const double ok = __shfl_xor_sync(0xffffffffu, key, o);
-    const int oe = __shfl_xor_sync(0xffffffffu, e, o);
-    if (ok > key || (ok == key && oe < e)) {
-      key = ok;
-      e = oe;
-    }
+// The warp's largest key and the lowest index that has it.  The high words decide unless two lanes
+// share the largest; one hardware reduction in place of five exchanges of key and index.
+__device__ __forceinline__ void warp_best(uint64_t& key, int& e) {
+  const uint32_t hi = static_cast<uint32_t>(key >> 32);
+  const uint32_t mh = __reduce_max_sync(0xffffffffu, hi);
+  unsigned who = __ballot_sync(0xffffffffu, hi == mh);
+  if (who & (who - 1)) {
+    const uint32_t lo = hi == mh ? static_cast<uint32_t>(key) : 0u;
+    const uint32_t ml = __reduce_max_sync(0xffffffffu, lo);
+    const bool mine = hi == mh && lo == ml;
+    const int me = __reduce_min_sync(0xffffffffu, mine ? e : 0x7fffffff);
+    key = (static_cast<uint64_t>(mh) << 32) | ml;
+    e = me;
+    return;
   }
+  const int src = __ffs(who) - 1;
+  key = __shfl_sync(0xffffffffu, key, src);
+  e = __shfl_sync(0xffffffffu, e, src);
 }
 
 template <int kIn, int PER>
 __global__ void __launch_bounds__(kRouteWarps * 32)
     route_kernel(const RouteArgs a) {
-  __shared__ double s_key[kRouteWarps][PER * 32];
+  __shared__ uint64_t s_key[kRouteWarps][PER * 32 + MAX_ROUTE_GROUPS];
   const int warp = threadIdx.x >> 5, lane = lane_id();
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
   if (t >= a.T) return;
   float x[PER];
-  double p[PER], key[PER];
+  double p[PER];
+  uint64_t key[PER];
   const bool good = route_scores<kIn, PER>(a, t, x, p);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = i * 32 + lane;
-    key[i] = neg_inf_d();
-    if (x[i] != __int_as_float(0xff800000))
-      key[i] = p[i] + (a.balance != nullptr ? static_cast<double>(__ldg(a.balance + e)) : 0.0);
-    if (!(key[i] == key[i])) key[i] = neg_inf_d();      // a NaN balance: never chosen
+    key[i] = 0ull;
+    if (x[i] != __int_as_float(0xff800000)) {
+      const double v = p[i] + (a.balance != nullptr ? static_cast<double>(__ldg(a.balance + e)) : 0.0);
+      if (v > __longlong_as_double(0xfff0000000000000ll)) key[i] = ordered(v);   // a NaN or -inf key: never chosen
+    }
   }
   if (a.groups > 1) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) s_key[warp][i * 32 + lane] = key[i];
-    __syncwarp();
     const int size = a.E / a.groups;
-    double total = neg_inf_d();
+    // one word of padding a group, so that the lanes, one a group, read different banks
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = i * 32 + lane;
+      if (e < a.E) s_key[warp][e + e / size] = key[i];
+    }
+    __syncwarp();
+    uint64_t total = 0ull;
     if (lane < a.groups) {
-      double b1 = neg_inf_d(), b2 = neg_inf_d();
+      uint64_t b1 = 0ull, b2 = 0ull;
       for (int j = 0; j < size; ++j) {
-        const double v = s_key[warp][lane * size + j];
+        const uint64_t v = s_key[warp][lane * (size + 1) + j];
         if (v > b1) {
           b2 = b1;
           b1 = v;
@@ -148,55 +168,80 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
         }
       }
       total = b1;
-      if (a.balance != nullptr && b2 > neg_inf_d()) total += b2;
+      if (a.balance != nullptr && b2 > 0ull) total = ordered(unordered(b1) + unordered(b2));
+      total = total > 1ull ? total : 1ull;              // a group of masked experts: below all others
     }
-    // a lane past the last group takes no part: its index loses every tie, its key is -inf
     unsigned kept = 0u;
-    double mine = total;
-    int id = lane < a.groups ? lane : 64 + lane;
+    int id = lane < a.groups ? lane : 64 + lane;        // a lane without a group: key 0, loses every tie
     for (int j = 0; j < a.top_groups; ++j) {
-      double b = mine;
+      uint64_t b = total;
       int g = id;
       warp_best(b, g);
       if (g < 32) kept |= 1u << g;
       if (g == id) {
-        mine = neg_inf_d();
-        id = 64 + lane;                                 // taken
+        total = 0ull;                                   // taken
+        id = 64 + lane;
       }
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int e = i * 32 + lane;
-      if (e < a.E && !((kept >> (e / size)) & 1u)) key[i] = neg_inf_d();
+      if (e < a.E && !((kept >> (e / size)) & 1u)) key[i] = 0ull;
     }
   }
-  double mine_p = 0.0, sum = 0.0;                       // lane j keeps choice j
-  int mine_e = -1;
+  // The scores by expert, for the lanes that will hold the choices; and the high words of the keys,
+  // which decide the order by themselves unless two are equal (keys within 2^-20 of one another).
+  __syncwarp();
+  double* score = reinterpret_cast<double*>(s_key[warp]);
+  uint32_t hi[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    score[i * 32 + lane] = p[i];
+    hi[i] = static_cast<uint32_t>(key[i] >> 32);
+  }
+  int mine_e = -1;                                      // lane j keeps choice j
   for (int j = 0; j < a.k; ++j) {
-    double b = neg_inf_d(), pb = 0.0;
-    int e = 0x7fffffff;
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) m = max(m, hi[i]);
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (m == 0u) {                                      // no key with a high word is left: dead, or the 1 of a dead group
+      break;
+    }
+    int at = 0, have = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (key[i] > b) {
-        b = key[i];
-        e = i * 32 + lane;
-        pb = p[i];
+      if (hi[i] == m) {
+        at = i;
+        ++have;
       }
-    const int own = e;
-    warp_best(b, e);
-    const bool found = b > neg_inf_d();
-    const double pw = __shfl_sync(0xffffffffu, pb, e & 31);
-    if (found && own == e) {
+    const unsigned who = __ballot_sync(0xffffffffu, have > 0);
+    int e;
+    if ((who & (who - 1)) == 0u && __ballot_sync(0xffffffffu, have > 1) == 0u) {
+      e = __shfl_sync(0xffffffffu, at * 32 + lane, __ffs(who) - 1);
+    } else {                                            // equal high words: the low ones, then the index
+      uint32_t lo = 0u;
 #pragma unroll
       for (int i = 0; i < PER; ++i)
-        if (i * 32 + lane == e) key[i] = neg_inf_d();
+        if (hi[i] == m) lo = max(lo, static_cast<uint32_t>(key[i]));
+      lo = __reduce_max_sync(0xffffffffu, lo);
+      int first = 0x7fffffff;
+#pragma unroll
+      for (int i = PER - 1; i >= 0; --i)
+        if (hi[i] == m && static_cast<uint32_t>(key[i]) == lo) first = i * 32 + lane;
+      e = __reduce_min_sync(0xffffffffu, first);
     }
-    if (found) sum += pw;
-    if (lane == j) {
-      mine_e = found ? e : -1;
-      mine_p = found ? pw : 0.0;
+    if (lane == (e & 31)) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (i == (e >> 5)) hi[i] = 0u;
     }
+    if (lane == j) mine_e = e;
   }
+  __syncwarp();
+  const double mine_p = mine_e >= 0 ? score[mine_e] : 0.0;
+  double sum = 0.0;                                     // in the order of the choices
+  for (int j = 0; j < a.k; ++j) sum += __shfl_sync(0xffffffffu, mine_p, j);
   if (lane < a.k) {
     double w = mine_p;
     if (a.renorm) w = sum > 0.0 ? mine_p / sum : 0.0;
@@ -288,8 +333,12 @@ __global__ void __launch_bounds__(kSortThreads)
   grid_dep_launch();
   if (e == 0)
     for (int i = threadIdx.x; i < zero_words; i += kSortThreads) zero[i] = 0u;
+  // every warp its own run of rows: counts, then positions, with one meeting of the CTA between
+  const int64_t per = ((R + kSortThreads - 1) / kSortThreads) * 32;
+  const int64_t r0 = warp * per, r1 = r0 + per < R ? r0 + per : R;
   int less = 0, eq = 0;
-  for (int64_t r = threadIdx.x; r < R; r += kSortThreads) {
+#pragma unroll 4
+  for (int64_t r = r0 + lane; r < r1; r += 32) {
     const int v = __ldg(idx + r);
     const bool in = v >= 0 && v < E;
     less += in && v < e;
@@ -307,34 +356,28 @@ __global__ void __launch_bounds__(kSortThreads)
     s_eq[warp] = eq;
   }
   __syncthreads();
-  int base = 0, total = 0;
+  int first = 0, total = 0, at = 0;
   for (int w = 0; w < kSortThreads / 32; ++w) {
-    base += s_less[w];
+    first += s_less[w];
     total += s_eq[w];
+    if (w < warp) at += s_eq[w];
   }
   if (threadIdx.x == 0) {
-    offsets[e] = base;
-    if (e == E - 1) offsets[E] = base + total;
+    offsets[e] = first;
+    if (e == E - 1) offsets[E] = first + total;
   }
-  if (total == 0) return;
-  for (int64_t r0 = 0; r0 < R; r0 += kSortThreads) {
-    const int64_t r = r0 + threadIdx.x;
-    const bool hit = r < R && __ldg(idx + r) == e;
+  if (eq == 0) return;
+  at += first;
+#pragma unroll 4
+  for (int64_t r = r0; r < r1; r += 32) {
+    const bool hit = r + lane < r1 && __ldg(idx + r + lane) == e;
     const unsigned bits = __ballot_sync(0xffffffffu, hit);
-    __syncthreads();                                    // the counts of the round before are read
-    if (lane == 0) s_eq[warp] = __popc(bits);
-    __syncthreads();
-    int before = 0, round = 0;
-    for (int w = 0; w < kSortThreads / 32; ++w) {
-      if (w < warp) before += s_eq[w];
-      round += s_eq[w];
-    }
     if (hit) {
-      const int at = base + before + __popc(bits & ((1u << lane) - 1u));
-      place[r] = at;
-      row_at[at] = static_cast<int32_t>(r);
+      const int to = at + __popc(bits & ((1u << lane) - 1u));
+      place[r + lane] = to;
+      row_at[to] = static_cast<int32_t>(r + lane);
     }
-    base += round;
+    at += __popc(bits);
   }
 }
 
@@ -442,20 +485,33 @@ __global__ void __launch_bounds__(256)
   if (t >= T) return;
   const int64_t c = (at - t * per) * 8;
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int j = 0; j < k; ++j) {
-    const int p = __ldg(place + t * k + j);
-    if (p < 0) continue;
-    const float w = weights != nullptr ? __ldg(weights + t * k + j) : 1.0f;
-    const float4 x = __ldg(reinterpret_cast<const float4*>(V + static_cast<int64_t>(p) * K + c));
-    const float4 y = __ldg(reinterpret_cast<const float4*>(V + static_cast<int64_t>(p) * K + c + 4));
-    s[0] = fmaf(w, x.x, s[0]);
-    s[1] = fmaf(w, x.y, s[1]);
-    s[2] = fmaf(w, x.z, s[2]);
-    s[3] = fmaf(w, x.w, s[3]);
-    s[4] = fmaf(w, y.x, s[4]);
-    s[5] = fmaf(w, y.y, s[5]);
-    s[6] = fmaf(w, y.z, s[6]);
-    s[7] = fmaf(w, y.w, s[7]);
+  for (int j0 = 0; j0 < k; j0 += 4) {               // four rows' loads in flight
+    int p[4];
+    float w[4];
+    float4 x[4], y[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      p[u] = j0 + u < k ? __ldg(place + t * k + j0 + u) : -1;
+      w[u] = p[u] < 0 ? 0.0f : weights != nullptr ? __ldg(weights + t * k + j0 + u) : 1.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (p[u] >= 0) {
+        x[u] = __ldg(reinterpret_cast<const float4*>(V + static_cast<int64_t>(p[u]) * K + c));
+        y[u] = __ldg(reinterpret_cast<const float4*>(V + static_cast<int64_t>(p[u]) * K + c + 4));
+      }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (p[u] >= 0) {
+        s[0] = fmaf(w[u], x[u].x, s[0]);
+        s[1] = fmaf(w[u], x[u].y, s[1]);
+        s[2] = fmaf(w[u], x[u].z, s[2]);
+        s[3] = fmaf(w[u], x[u].w, s[3]);
+        s[4] = fmaf(w[u], y[u].x, s[4]);
+        s[5] = fmaf(w[u], y[u].y, s[5]);
+        s[6] = fmaf(w[u], y[u].z, s[6]);
+        s[7] = fmaf(w[u], y[u].w, s[7]);
+      }
   }
   *reinterpret_cast<uint4*>(out + t * K + c) =
       make_uint4(blk::pack2<kBf16>(s[0], s[1]), blk::pack2<kBf16>(s[2], s[3]), blk::pack2<kBf16>(s[4], s[5]), blk::pack2<kBf16>(s[6], s[7]));

@@ -1088,7 +1088,7 @@ i8_status i8_block_quantize_weight(const void* W, int32_t dtype, int64_t Z, int6
 
 size_t i8_block_linear_workspace_size(int64_t T, int64_t N, int64_t K) {
   if (!shape_ok(T, K) || !fits_int(N)) return 0;
-  return linear_ws(T, K).total;
+  return linear_ws(T, N, K).total;
 }
 
 i8_status i8_block_linear_forward(const void* X, int32_t dtype, int64_t T, int64_t K, const uint8_t* CB,
@@ -1098,7 +1098,7 @@ i8_status i8_block_linear_forward(const void* X, int32_t dtype, int64_t T, int64
       !aligned16(bias) || !aligned16(Y) || !aligned16(workspace))
     return I8_ERR_INVALID_ARG;
   if (!dtype16(dtype) || !shape_ok(T, K) || !fits_int(N)) return I8_ERR_INVALID_ARG;
-  if (workspace_bytes < linear_ws(T, K).total) return I8_ERR_INVALID_ARG;
+  if (workspace_bytes < linear_ws(T, N, K).total) return I8_ERR_INVALID_ARG;
   DeviceInfo* d;
   i8_status st = device_info(&d);
   if (st != I8_OK) return st;

@@ -4,7 +4,6 @@
 #pragma once
 
 constexpr int kPartGrid = 160;                // CTAs that the workspace of a split product allows for
-constexpr int64_t kSkinnyMaxT = 128;          // rows up to which the product streams the weight
 
 bool dtype16(int32_t dt) { return dt == I8_DTYPE_F16 || dt == I8_DTYPE_BF16; }
 bool fits_int(int64_t v) { return v > 0 && v <= 0x7fffffffLL; }
@@ -55,8 +54,7 @@ SkinnyFn skinny_fn(int nt, int out, int in) {
     return out == blk::kOutF32 ? block_skinny_kernel<16, blk::kOutF32, kInBf16> : block_skinny_kernel<16, blk::kOutBf16, kInBf16>;
   switch (nt) {
     case 32: return skinny_fn_nt<32>(out);
-    case 64: return skinny_fn_nt<64>(out);
-    default: return skinny_fn_nt<128>(out);
+    default: return skinny_fn_nt<64>(out);
   }
 }
 
@@ -102,7 +100,7 @@ i8_status block_info(const DeviceInfo& d, BlockInfo** out) {
       clusters = clusters == 0 || c < clusters ? c : clusters;
     }
     for (int o = blk::kOutF16; o <= blk::kOutF32; ++o) {
-      for (int nt = 32; nt <= 128; nt *= 2)
+      for (int nt = 32; nt <= 64; nt *= 2)
         if (!cuda_ok(cudaFuncSetAttribute(skinny_fn(nt, o, skinny::kInCodes), smem_attr, static_cast<int>(skinny::smem_bytes(nt))),
                      "cudaFuncSetAttribute(block skinny)"))
           return I8_ERR_CUDA;
@@ -196,7 +194,14 @@ i8_status run_skinny(int nt, int out, int in, const CUtensorMap& tW, const CUten
   return cuda_ok(e, "kernel launch") ? launch_status() : I8_ERR_CUDA;
 }
 
-int skinny_tokens(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+int skinny_tokens(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+// Whether a linear layer streams its weight (block_skinny.cuh) or takes the 256 x 256 tiles: up to
+// 16 tokens always; up to 64 when the weight has more tiles of 256 outputs than there are CTA
+// pairs, so that the tiles would leave SMs idle in their last round.  T = 32: 4096 -> 16384 (64
+// tiles) 26 us streaming, 21 us in tiles; 14336 -> 28672 (112 tiles) 83 and 105 us; T = 96 there:
+// 116 and 114 us.
+bool streams(int64_t T, int64_t N) { return T <= 16 || (T <= 64 && (N + blk::TN - 1) / blk::TN > kPartGrid / 2); }
 size_t parts_bytes(int nt) { return static_cast<size_t>(2 * kPartGrid) * static_cast<size_t>(nt) * 128u * 4u; }
 
 struct Taker {
@@ -212,14 +217,14 @@ struct Taker {
 struct LinearWs {
   size_t xq, sx, arrived, parts, total;
 };
-LinearWs linear_ws(int64_t T, int64_t K) {
+LinearWs linear_ws(int64_t T, int64_t N, int64_t K) {
   LinearWs w{};
   Taker take;
   if (T > 16) {
     w.xq = take(T * K);
     w.sx = take(blocks128(K) * T * 4);
   }
-  if (T <= kSkinnyMaxT) {
+  if (streams(T, N)) {
     w.arrived = take(kPartGrid * 4);
     w.parts = take(static_cast<int64_t>(parts_bytes(skinny_tokens(T))));
   }
@@ -233,8 +238,8 @@ i8_status block_linear_forward(const void* X, int32_t dtype, int64_t T, int64_t 
   BlockInfo* b;
   i8_status st = block_info(d, &b);
   if (st != I8_OK) return st;
-  const LinearWs w = linear_ws(T, K);
-  const bool few = T <= kSkinnyMaxT, direct = T <= 16;
+  const LinearWs w = linear_ws(T, N, K);
+  const bool few = streams(T, N), direct = T <= 16;
   const bool bf = dtype == I8_DTYPE_BF16;
   blk::QuantArgs q = quant_args(X, T, K);
   q.Qr = ws + w.xq;
@@ -441,11 +446,10 @@ bool experts_shape(int64_t T, int64_t K, int64_t I, int64_t E, int64_t k, Expert
   return true;
 }
 
-// tokens of a tile when the experts' rows are few on average, 0 when the wide product is used
-int experts_tokens(const ExpertsShape& x) {
-  const int64_t mean = (x.R + x.E - 1) / x.E;
-  return mean <= 64 ? skinny_tokens(mean) : 0;
-}
+// Whether the experts' rows are so few on average that their products stream the weights in tiles
+// of 16 rows.  64 experts of 4096 x 1024, 8 a token, in us streaming / in 256-row tiles: 4 rows an
+// expert 169 / 214, 8 rows 210 / 226, 16 rows 296 / 237.
+bool experts_stream(const ExpertsShape& x) { return x.R <= 8 * x.E; }
 
 struct ExpertsWs {
   size_t offsets, place, row_at, xq, sx, arrived, parts, gu, h, sh, y, total;
@@ -453,18 +457,17 @@ struct ExpertsWs {
 ExpertsWs experts_ws(const ExpertsShape& x, bool backward) {
   ExpertsWs w{};
   Taker take;
-  const int nt = experts_tokens(x);
+  const bool direct = !backward && experts_stream(x);
   w.offsets = take((x.E + 1) * 4);
   w.place = take(x.R * 4);
   w.row_at = take(x.R * 4);
-  const bool direct = !backward && nt == 16;
   if (!direct) {
     w.xq = take(x.R * x.K);                    // rows of x, or of dy, by expert
     w.sx = take(static_cast<int64_t>(x.KB) * x.R * 4);
   }
   w.arrived = take(2 * kPartGrid * 4);
-  if (!backward && nt > 0) {
-    w.parts = take(static_cast<int64_t>(parts_bytes(nt)));
+  if (direct) {
+    w.parts = take(static_cast<int64_t>(parts_bytes(16)));
     w.gu = take(x.R * 2 * x.I * 4);
   }
   if (backward) w.gu = take(x.R * x.I * 4);    // dy W2
@@ -513,8 +516,7 @@ i8_status experts_forward(const void* X, int32_t dtype, const int32_t* idx, cons
   i8_status st = block_info(d, &b);
   if (st != I8_OK) return st;
   const ExpertsWs w = experts_ws(x, false);
-  const int nt = experts_tokens(x);
-  const bool direct = nt == 16;                // the products form the codes of their rows
+  const bool direct = experts_stream(x);      // the products form the codes of their rows
   st = experts_rows(X, dtype, idx, x, w, ws, nullptr, !direct, s);
   if (st != I8_OK) return st;
   const int32_t* offsets = reinterpret_cast<const int32_t*>(ws + w.offsets);
@@ -524,13 +526,10 @@ i8_status experts_forward(const void* X, int32_t dtype, const int32_t* idx, cons
   float* Y2 = reinterpret_cast<float*>(ws + w.y);
   unsigned int* arrived = reinterpret_cast<unsigned int*>(ws + w.arrived);
   CUtensorMap tX, tW13, tH, tW2;
-  if (nt > 0) {
+  if (direct) {
     float* gu = GU != nullptr ? GU : reinterpret_cast<float*>(ws + w.gu);
-    const int64_t token_tiles = x.R / nt + (x.R < x.E ? x.R : x.E);   // at most
+    const int64_t token_tiles = x.R / 16 + (x.R < x.E ? x.R : x.E);   // at most
     if (!map_codes(&tW13, CB13, x.K, x.I, 2 * x.E, x.K, skinny::ROWS) || !map_codes(&tW2, CB2, x.I, x.K, x.E, x.I, skinny::ROWS))
-      return I8_ERR_CUDA;
-    tX = tH = tW2;
-    if (!direct && (!map_codes(&tX, ws + w.xq, x.K, x.R, 0, x.K, nt) || !map_codes(&tH, ws + w.h, x.Ip, x.R, 0, x.Ip, nt)))
       return I8_ERR_CUDA;
     skinny::Args a = {};
     a.X = X;
@@ -545,35 +544,24 @@ i8_status experts_forward(const void* X, int32_t dtype, const int32_t* idx, cons
     a.n_tiles = 2 * x.IB;
     a.z_cols = static_cast<int>(x.I);
     a.z_per_group = 2;
-    a.SA = SX;
     a.SB = S13;
     a.C = gu;
     a.ldc = 2 * x.I;
     a.parts = reinterpret_cast<float*>(ws + w.parts);
     a.arrived = arrived;
-    const int in = !direct ? skinny::kInCodes : dtype == I8_DTYPE_BF16 ? skinny::kInBf16 : skinny::kInF16;
-    st = run_skinny(nt, blk::kOutF32, in, tW13, tX, a, token_tiles, d, s);
+    st = run_skinny(16, blk::kOutF32, dtype == I8_DTYPE_BF16 ? skinny::kInBf16 : skinny::kInF16, tW13, tW13, a, token_tiles, d, s);
     if (st != I8_OK) return st;
-    if (!direct) {
-      const int64_t warps = x.R * x.IB, grid = (warps + 7) / 8;
-      if (!fits_int(grid)) return I8_ERR_INVALID_ARG;
-      const cudaError_t e = launch_overlapped(moe::gated_quant_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s,
-                                              static_cast<const float*>(gu), offsets + x.E, x.R, static_cast<int>(x.I),
-                                              ws + w.h, x.Ip, SH);
-      if (!cuda_ok(e, "kernel launch") || launch_status() != I8_OK) return I8_ERR_CUDA;
-    }
     a.X = gu;
     a.k_cols = x.I;
     a.k_blocks = x.IB;
     a.n_tiles = a.n_per_z = x.KB;
     a.z_cols = static_cast<int>(x.K);
     a.z_per_group = 1;
-    a.SA = SH;
     a.SB = S2;
     a.C = Y2;
     a.ldc = x.K;
     a.arrived = arrived + kPartGrid;
-    st = run_skinny(nt, blk::kOutF32, direct ? skinny::kInGated : skinny::kInCodes, tW2, tH, a, token_tiles, d, s);
+    st = run_skinny(16, blk::kOutF32, skinny::kInGated, tW2, tW2, a, token_tiles, d, s);
   } else {
     const int64_t m_tiles = x.R / blk::TM + (x.R < x.E ? x.R : x.E);
     if (!map_codes(&tX, ws + w.xq, x.K, x.R, 0, x.K, blk::HM) || !map_codes(&tW13, CB13, x.K, x.I, 2 * x.E, x.K, 64) ||

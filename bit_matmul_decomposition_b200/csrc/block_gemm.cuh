@@ -183,6 +183,26 @@ __device__ __forceinline__ float fast_sigmoid(float g) {
   return __fdividef(1.0f, 1.0f + e);
 }
 
+// 16 fp32 columns (a thread its row's) of a warp's 32 rows through 2 KB of shared memory, so that
+// four lanes write 64 bytes of one row; written by themselves, a thread's 16 bytes lie a row apart
+// from the next thread's.  rows: how many of the 32 exist; columns from n on (a multiple of 4) do not.
+__device__ __forceinline__ void store16_f32(uint32_t stage, const float* v, float* base, int64_t ld, int col, int n, int rows) {
+  const int lane = lane_id();
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    gemm::sts_v4(stage + static_cast<uint32_t>(lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)), __float_as_uint(v[4 * j]),
+                 __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+  __syncwarp();
+  const int j = lane & 3, c = col + 4 * j;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    const uint4 x = lds_v4(stage + static_cast<uint32_t>(r * 64 + ((j ^ ((r >> 1) & 3)) << 4)));
+    if (r < rows && c < n) *reinterpret_cast<uint4*>(base + static_cast<int64_t>(r) * ld + c) = x;
+  }
+}
+
 // position of tile t of a group of m_tiles x n_tiles: GROUP_M m-tiles, then the next n-tile
 __device__ __forceinline__ void raster(int t, int m_tiles, int n_tiles, int& mt, int& nt) {
   const int G = m_tiles < GROUP_M ? m_tiles : GROUP_M;
@@ -563,15 +583,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // acc[0..63] = g, acc[64..127] = u of features i0 .. i0 + 63
         const int i0 = nt * HN + half * 64;
         float am = 0.0f;
-        if (a.GU != nullptr && row_ok && !dead) {
+        if (a.GU != nullptr && !dead) {
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            float* dst = a.GU + (static_cast<int64_t>(row) * 2 + w) * a.Nc + i0;
-#pragma unroll
-            for (int j = 0; j < 64; j += 4)          // Nc % 16 == 0: four features stay together
-              if (i0 + j < a.Nc)
-                *reinterpret_cast<float4*>(dst + j) = make_float4(acc[w * 64 + j], acc[w * 64 + j + 1], acc[w * 64 + j + 2], acc[w * 64 + j + 3]);
-          }
+          for (int j = 0; j < 128; j += 16)
+            store16_f32(cst, &acc[j], a.GU + static_cast<int64_t>(wrow0) * 2 * a.Nc + (j >> 6) * a.Nc, 2 * static_cast<int64_t>(a.Nc),
+                        i0 + (j & 63), a.Nc, row_end - wrow0);
         }
 #pragma unroll
         for (int j = 0; j < 64; ++j) {
@@ -602,28 +618,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const int c0 = n0 + c * 32;
           if (c0 >= a.Nc) continue;
           if (kOut == kOutF32) {
-            // 16 columns of the 32 rows at a time through shared memory, so that four lanes write
-            // 64 bytes of one row (a thread's own row alone is 16 bytes a store, 32 rows apart)
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              const int c1 = c0 + w * 16;
-              __syncwarp();
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int e = c * 32 + w * 16 + 4 * j;
-                gemm::sts_v4(cst + static_cast<uint32_t>(lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)), __float_as_uint(acc[e]),
-                             __float_as_uint(acc[e + 1]), __float_as_uint(acc[e + 2]), __float_as_uint(acc[e + 3]));
-              }
-              __syncwarp();
-              const int j = lane & 3, col = c1 + 4 * j;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int r = i * 8 + (lane >> 2);
-                const uint4 v = lds_v4(cst + static_cast<uint32_t>(r * 64 + ((j ^ ((r >> 1) & 3)) << 4)));
-                if (wrow0 + r < row_end && col < a.Nc)         // Nc % 16 == 0 in this form
-                  *reinterpret_cast<uint4*>(static_cast<float*>(a.C) + static_cast<int64_t>(wrow0 + r) * a.ldc + col) = v;
-              }
-            }
+            for (int w = 0; w < 2; ++w)
+              store16_f32(cst, &acc[c * 32 + w * 16], static_cast<float*>(a.C) + static_cast<int64_t>(wrow0) * a.ldc, a.ldc,
+                          c0 + w * 16, a.Nc, row_end - wrow0);
             continue;
           }
           uint32_t o[16];

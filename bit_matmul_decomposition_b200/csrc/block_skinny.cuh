@@ -4,7 +4,7 @@
 //   C[t,n] = sum_b SA[b, t] * SB[b, n/128] * ( sum_{r in block b} A(t,r) * B(n,r) )
 //
 // The roles of the operands are swapped: 128 rows of the weight are the tensor cores' M, and
-// NT = 16..128 tokens their N, so that one token costs an MMA of N = 16 and not of M = 128.
+// NT = 16..64 tokens their N, so that one token costs an MMA of N = 16 and not of M = 128.
 // TMEM lanes are then output features and columns tokens; the weight's scale is one number for
 // a whole tile and block, the tokens' scales differ by column and come through shared memory.
 //
@@ -13,7 +13,8 @@
 // CTA, whatever tile they fall in.  A tile that one CTA ran alone is written at once; the
 // others leave fp32 partial sums in the workspace, and the CTA that arrives last (a counter)
 // adds the parts of the tile in the order of the CTAs and writes it: the order of arrival
-// changes nothing in the result, and no CTA waits for another.
+// changes nothing in the result, and no CTA waits for another.  Where whole tiles fill the SMs
+// well enough by themselves, none is split.
 //
 // Design (sm_100a): one CTA an SM; warp 0 fills a ring of [128 x 128 weight | NT x 128 token]
 // stages by TMA, warp 1 issues tcgen05.mma (cta_group::1, kind::f8f6f4, M = 128, N = NT), one
@@ -38,6 +39,8 @@ constexpr int PRE_BYTES = blk::PRE_BYTES;
 constexpr int BAR_BYTES = 1024;
 constexpr int MAX_STAGES = 12;
 constexpr int NBUF = 4;                      // TMEM accumulators
+constexpr int MIN_UNITS = 8;                 // units of a CTA: joining a tile's parts costs about as much
+                                             // (4096 -> 4096, one token: 12.7 us; with 4: 15.0)
 constexpr int RING_BUDGET = 210 * 1024;
 
 __host__ __device__ constexpr int stage_bytes(int nt) { return W_BYTES + nt * BK; }
@@ -49,8 +52,7 @@ __host__ __device__ constexpr int scale_bytes(int nt) { return SLOTS * nt * 4; }
 __host__ __device__ constexpr size_t smem_bytes(int nt) {
   return static_cast<size_t>(stages(nt)) * stage_bytes(nt) + scale_bytes(nt) + PRE_BYTES + BAR_BYTES + 1024;
 }
-static_assert(smem_bytes(16) <= 232448 && smem_bytes(32) <= 232448 && smem_bytes(64) <= 232448 &&
-              smem_bytes(128) <= 232448, "shared memory per CTA");
+static_assert(smem_bytes(16) <= 232448 && smem_bytes(32) <= 232448 && smem_bytes(64) <= 232448, "shared memory per CTA");
 
 // Where the tokens' codes come from: the quantiser's, by TMA; or, for tiles of 16 tokens, formed in
 // the kernel by eight warps that take the units in turn and write codes and scales straight into
@@ -224,10 +226,15 @@ __global__ void __launch_bounds__(threads(kIn), 1)
 
   const int KB = a.k_blocks;
   const int64_t units = static_cast<int64_t>(__shfl_sync(0xffffffffu, pre[a.groups], 0)) * a.n_tiles * KB;
-  // G CTAs share the units, each at least one: with fewer units than CTAs (known only here, by
-  // the groups' sizes) the CTAs past the last unit have none and take no part in any tile
-  const int64_t G = units < static_cast<int64_t>(gridDim.x) ? units : static_cast<int64_t>(gridDim.x);
-  auto first_unit = [&](int64_t c) -> int64_t { return units * c / G; };
+  // How many units there are is known only here, by the groups' sizes.  Where whole tiles, dealt out
+  // to the CTAs in turn, keep at least 85 in 100 of them busy to the end, no tile is split;
+  // otherwise G CTAs share the units, each at least MIN_UNITS unless there are fewer in all.
+  // CTAs past the last take no part in any tile.
+  const int64_t tiles = units / KB, grid = gridDim.x;
+  const bool whole = tiles > 0 && tiles * 100 >= (tiles + grid - 1) / grid * grid * 85;
+  const int64_t most = whole ? tiles : units / MIN_UNITS > 0 ? units / MIN_UNITS : (units > 0 ? 1 : 0);
+  const int64_t G = most < grid ? most : grid;
+  auto first_unit = [&](int64_t c) -> int64_t { return whole ? tiles * c / G * KB : units * c / G; };
   const bool idle = static_cast<int64_t>(blockIdx.x) >= G;
   const int64_t u0 = idle ? 0 : first_unit(blockIdx.x);
   const int64_t u1 = idle ? 0 : first_unit(static_cast<int64_t>(blockIdx.x) + 1);
@@ -553,11 +560,22 @@ __global__ void __launch_bounds__(threads(kIn), 1)
           __threadfence();
 #pragma unroll
           for (int j = 0; j < NT; ++j) acc[j] = 0.0f;
-          for (int64_t c = c0; c <= c1; ++c) {
-            const float* p = a.parts + slot(c) * (NT * ROWS) + nl;
+          // in the order of the CTAs; JOIN parts' loads in flight
+          constexpr int JOIN = NT <= 16 ? 4 : NT <= 32 ? 2 : 1;
+          for (int64_t c = c0; c <= c1; c += JOIN) {
+            float v[JOIN][NT];
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-              if (row0 + j < row_end) acc[j] += __ldcg(p + j * ROWS);
+            for (int i = 0; i < JOIN; ++i) {
+              const float* p = a.parts + slot(c + i <= c1 ? c + i : c1) * (NT * ROWS) + nl;
+#pragma unroll
+              for (int j = 0; j < NT; ++j) v[i][j] = row0 + j < row_end ? __ldcg(p + j * ROWS) : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < JOIN; ++i)
+              if (c + i <= c1) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) acc[j] += v[i][j];
+              }
           }
         }
       }

@@ -382,36 +382,6 @@ __global__ void __launch_bounds__(kSortThreads)
 }
 
 // ------------------------------------------------------------------ gated activation
-// h = silu(g) * u of GU [R][2][I] (fp32) as row codes [R][h_pitch] and scales [ceil(I/128)][R];
-// one warp a block of 128 features.  Rows past the last expert's are left alone.
-__global__ void __launch_bounds__(256)
-    gated_quant_kernel(const float* __restrict__ GU, const int32_t* __restrict__ rows_end, int64_t R, int I,
-                       uint8_t* __restrict__ H, int64_t h_pitch, float* __restrict__ SH) {
-  grid_dep_wait();
-  grid_dep_launch();
-  const int blocks = (I + blk::QB - 1) / blk::QB;
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
-  const int64_t row = w / blocks;
-  const int b = static_cast<int>(w - row * blocks);
-  if (row >= __ldg(rows_end)) return;
-  const int i = b * blk::QB + lane_id() * 4;
-  float h[4] = {0.f, 0.f, 0.f, 0.f};
-  if (i < I) {
-    const float4 g = __ldg(reinterpret_cast<const float4*>(GU + (row * 2) * I + i));
-    const float4 u = __ldg(reinterpret_cast<const float4*>(GU + (row * 2 + 1) * I + i));
-    h[0] = g.x * blk::fast_sigmoid(g.x) * u.x;
-    h[1] = g.y * blk::fast_sigmoid(g.y) * u.y;
-    h[2] = g.z * blk::fast_sigmoid(g.z) * u.z;
-    h[3] = g.w * blk::fast_sigmoid(g.w) * u.w;
-  }
-  float am = fmaxf(fmaxf(fabsf(h[0]), fabsf(h[1])), fmaxf(fabsf(h[2]), fabsf(h[3])));
-  am = fmaxf(warp_max(am), blk::kScaleFloor);
-  const float up = blk::block_up(am);
-  const uint32_t q = e4m3x2(h[0] * up, h[1] * up) | (static_cast<uint32_t>(e4m3x2(h[2] * up, h[3] * up)) << 16);
-  *reinterpret_cast<uint32_t*>(H + row * h_pitch + i) = q;
-  if (lane_id() == 0) SH[static_cast<int64_t>(b) * R + row] = blk::block_down(am);
-}
-
 // Gradient of a row's activation.  dH [R][I] is dy W2 without the row's weight w:
 //   dw = sum_i dH_i h_i;   dg = w dH u s (1 + g (1 - s)),  du = w dH g s,  s = sigmoid(g)
 // dg and du leave as row codes [R][2 * h_pitch] and scales [2 * ceil(I/128)][R].  One CTA a row;

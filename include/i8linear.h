@@ -364,7 +364,8 @@ i8_status i8_igemm_s32(const int8_t* A, int64_t T, int64_t K, const int8_t* B, i
  *   blocks are fp32; one rounding to dtype at the end.  bias may be NULL.  workspace: at least
  *   i8_block_linear_workspace_size(T, N, K) bytes, contents need no initialisation (calls
  *   sharing it must be ordered on one stream).
- *   T <= 128 streams the weight once over all SMs; more rows take 256 x 256 tiles.
+ *   T <= 16 (and T <= 64 for wide layers) streams the weight once over all SMs; more rows take
+ *   256 x 256 tiles.
  * i8_block_linear_backward(dY, X, dtype, T, N, K, CB, SCB, dX, dW, db, workspace, bytes, stream):
  *   the gradients of y = x W^T + b passed straight through the quantisation, for the outputs
  *   that are not NULL:

@@ -110,7 +110,7 @@ __device__ __forceinline__ void epi_bar256() { asm volatile("bar.sync 1, 256;" :
 // Arrive on the pair leader's barrier, ordered as the reads of TMEM before it are (they have
 // completed: tcgen05.wait::ld, then the tcgen05 fence).  The release is at CTA scope: nothing in
 // memory is handed over, and a release at cluster scope waits for the thread's outstanding
-// memory operations every time (the warps' largest stall: 2.78 ms against X ms at
+// memory operations every time (it was the warps' largest stall: 2.78 ms against 1.71 at
 // 2048 x 12288 x 49152).
 __device__ __forceinline__ void arrive_leader(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");

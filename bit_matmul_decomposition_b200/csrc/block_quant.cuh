@@ -13,8 +13,8 @@
 //
 // One CTA of 256 threads holds a 128 x 128 tile of the input in registers (eight 16-byte
 // groups a thread, all in flight at once; 32 rows where only row codes are wanted), so one read of the input gives any of: its row
-// codes, its tile codes, its column sums.  The pass is bound by HBM: 2 bytes read and 1 written
-// per value and code set.
+// codes, its tile codes, its column sums.  The pass is bound by HBM, 2 bytes read and 1 written
+// per value and code set: a 16384 x 4096 weight takes 39 us, 5.2 TB/s.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -113,7 +113,7 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
 }
 
 // PASSES: rows of 16 a thread holds; 8 for tiles, 2 when row codes alone are wanted (four times the
-// CTAs: 2048 x 4096 took X us with 128 rows a CTA, Y us with 32).
+// CTAs: 2048 x 4096 takes 8.4 us, with 128 rows a CTA 9.4; 333 x 4112 3.3 and 6.3).
 template <bool kBf16, bool kRows, bool kTiles, int PASSES>
 __global__ void __launch_bounds__(kQuantThreads, PASSES == 2 ? 6 : kRows && kTiles ? 3 : 4)
     block_quant_kernel(const QuantArgs a) {
@@ -169,11 +169,17 @@ __global__ void __launch_bounds__(kQuantThreads, PASSES == 2 ? 6 : kRows && kTil
       const uint2 q = codes8_scaled(f, block_up(am));
       const float down = block_down(am);
       const int n = a.dest != nullptr ? a.copies : 1;
-      for (int j = 0; j < n; ++j) {
-        const int64_t t = a.dest != nullptr ? __ldg(a.dest + r * a.copies + j) : r;
-        if (t < 0) continue;
-        if (c0 < a.qr_pitch) *reinterpret_cast<uint2*>(a.Qr + t * a.qr_pitch + c0) = q;
-        if ((threadIdx.x & 15) == 0) a.Sr[cb * a.rows_out + t] = down;
+      for (int j0 = 0; j0 < n; j0 += 4) {            // four places' loads in flight
+        int64_t t[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          t[j] = j0 + j >= n ? -1 : a.dest != nullptr ? __ldg(a.dest + r * a.copies + j0 + j) : r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (t[j] < 0) continue;
+          if (c0 < a.qr_pitch) *reinterpret_cast<uint2*>(a.Qr + t[j] * a.qr_pitch + c0) = q;
+          if ((threadIdx.x & 15) == 0) a.Sr[cb * a.rows_out + t[j]] = down;
+        }
       }
     }
   }

@@ -368,3 +368,46 @@ def test_replace_and_state_dict(tmp_path):
     n = B.LinearBlockFp8(128, 200, device=DEV)
     n.load_state_dict(torch.load(tmp_path / "l.pt"))
     assert torch.equal(n(x.to(DEV)), y)
+
+
+# ------------------------------------------------------------------ sizes past 32 bits
+def test_a_weight_of_more_than_2_31_codes():
+    """The last rows of the weight repeat the first: so do the last columns of the output."""
+    K, N = 20480, 106000                                  # 2.17e9 codes
+    g = torch.Generator(device=DEV).manual_seed(1)
+    codes = torch.empty((N, K), dtype=torch.uint8, device=DEV)
+    for i in range(0, N, 10600):
+        codes[i:i + 10600] = torch.randint(0, 256, (10600, K), generator=g, device=DEV, dtype=torch.uint8) & 0xBF
+    tail = N - 256 - (N % 128)                            # whole tiles, so that the scales can repeat too
+    codes[tail:tail + 256] = codes[:256]
+    scales = torch.rand(((N + 127) // 128, K // 128), generator=g, device=DEV)
+    scales[tail // 128:tail // 128 + 2] = scales[:2]
+    for T in (2, 40, 130):                                # both forms of the product
+        x = _x(T, K, torch.bfloat16).to(DEV)
+        y = B.linear_block_fp8(x, codes, scales)
+        assert torch.isfinite(y).all() and torch.equal(y[:, tail:tail + 256], y[:, :256])
+        del x, y
+    xv, wv = R.rows_value(_x(2, K, torch.bfloat16)), R.codes_value(codes[tail:tail + 8], scales[tail // 128:tail // 128 + 1])
+    ref = xv @ wv.T
+    got = B.linear_block_fp8(_x(2, K, torch.bfloat16).to(DEV), codes, scales)[:, tail:tail + 8]
+    R.check(got, ref, R.product_bound(xv, wv, torch.bfloat16, ref, K))
+
+
+def test_activations_and_gradients_of_more_than_2_31_elements():
+    T, K, N = 135000, 16384, 16                           # x: 2.2e9 elements
+    w = (torch.randn(N, K) * 0.05).to(torch.bfloat16).to(DEV).requires_grad_(True)
+    x = torch.empty((T, K), dtype=torch.bfloat16, device=DEV)
+    for i in range(0, T, 13500):
+        x[i:i + 13500] = torch.randn(13500, K, device=DEV)
+    x[-300:] = x[:300]
+    x.requires_grad_(True)
+    y = B.linear_block_fp8_train(x, w)
+    assert torch.equal(y[-300:], y[:300])
+    dy = torch.randn(T, N, device=DEV).to(torch.bfloat16)
+    dy[-300:] = dy[:300]
+    y.backward(dy)
+    assert torch.equal(x.grad[-300:], x.grad[:300])
+    gv, wv = R.rows_value(dy[-5:].cpu()), R.tiles_value(w.detach().cpu())
+    ref = gv @ wv
+    R.check(x.grad[-5:], ref, R.product_bound(gv, wv.T, torch.bfloat16, ref, N))
+    assert torch.isfinite(w.grad).all()

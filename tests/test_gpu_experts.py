@@ -242,3 +242,68 @@ def test_from_linears_and_state_dict(tmp_path):
     n.load_state_dict(torch.load(tmp_path / "e.pt"))
     assert torch.equal(n(x.to(DEV), idx.to(DEV), w.to(DEV)).view(2, 5, 128), y)
     assert m(x[:0].to(DEV), idx[:0].to(DEV), w[:0].to(DEV)).shape == (0, 128)
+
+
+@pytest.mark.parametrize("T", [6, 700])
+def test_calls_beside_one_another_on_two_streams(T):
+    """Each call has its own counters and partial tiles: interleaved calls change nothing."""
+    cases = [_case(T, 4, 2, 512, 272, torch.bfloat16, seed=s) for s in (1, 2)]
+    codes, *_ = _codes(cases[0][1], cases[0][2])
+    args = [(c[0].to(DEV), c[3].to(DEV), c[4].to(DEV)) for c in cases]
+    want = [X.experts_block_fp8(x, i, w, *codes) for x, i, w in args]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k].append(X.experts_block_fp8(*args[k], *codes))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for y in got[k]:
+            assert torch.equal(y, want[k])
+
+
+def test_backward_captured_while_an_eager_graph_lives():
+    x, w13, w2, idx, w, dy = _case(50, 4, 2, 256, 144, torch.bfloat16)
+    codes, *_ = _codes(w13, w2)
+    leaves = [x.to(DEV).requires_grad_(True), w.to(DEV).requires_grad_(True)]
+    idd, dyd = idx.to(DEV), dy.to(DEV)
+    eager = X.experts_block_fp8(leaves[0], idd, leaves[1], *codes)
+    own = [v.detach().clone().requires_grad_(True) for v in leaves]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(X.experts_block_fp8(own[0], idd, own[1], *codes), own, dyd)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        grads = torch.autograd.grad(X.experts_block_fp8(own[0], idd, own[1], *codes), own, dyd)
+    g.replay()
+    want = torch.autograd.grad(eager, leaves, dyd)
+    torch.cuda.synchronize()
+    for a, c in zip(grads, want):
+        assert torch.equal(a, c)
+
+
+def test_gradients_against_differences():
+    """dw by central differences of the layer itself (it is linear in the weights); dx along a
+    direction that the codes hold: see the linear layer's test for the products."""
+    x, w13, w2, idx, w, dy = _case(12, 3, 2, 128, 128, torch.bfloat16, none=0.0)
+    codes, W1, W3, W2 = _codes(w13, w2)
+    wd = w.to(DEV).requires_grad_(True)
+    X.experts_block_fp8(x.to(DEV), idx.to(DEV), wd, *codes).backward(dy.to(DEV))
+    for t, j in ((0, 0), (5, 1), (11, 0)):
+        up, down = w.clone(), w.clone()
+        up[t, j] += 0.5
+        down[t, j] -= 0.5
+        # the formula's dw uses q(dy); the differences take the same
+        fu, fd = (R.experts(x, idx, v, W1, W3, W2) for v in (up, down))
+        slope = float(((fu - fd) * R.rows_value(dy)).sum())
+        # dw stands for h, unquantised; the layer's output for q(h): 2^-4 of each of its terms
+        e = int(idx[t, j])
+        xq = R.rows_value(x)[t]
+        g, u = W1[e] @ xq, W3[e] @ xq
+        h = g * torch.sigmoid(g) * u
+        terms = (R.rows_value(dy)[t] @ W2[e]) * h
+        assert abs(float(wd.grad[t, j]) - slope) <= 2.0 ** -4 * float(terms.abs().sum()) + 1e-6

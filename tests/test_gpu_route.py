@@ -152,3 +152,15 @@ def test_strides_shapes_streams_and_capture():
     xd.copy_(other)
     g.replay()
     assert torch.equal(i3.cpu(), R.route(other, 4, None, "softmax", 1, 1, True, 1.0)[1])
+
+
+def test_more_than_2_31_logits():
+    T, E = 4200000, 512
+    x = torch.empty((T, E), dtype=torch.bfloat16, device=DEV)
+    for i in range(0, T, 420000):
+        x[i:i + 420000] = torch.randn(420000, E, device=DEV)
+    x[-100:] = x[:100]
+    w, idx = route_experts(x, 4, score="sigmoid")
+    assert torch.equal(w[-100:], w[:100]) and torch.equal(idx[-100:], idx[:100])
+    rw, ri, _ = R.route(x[-3:].cpu(), 4, None, "sigmoid", 1, 1, True, 1.0)
+    assert torch.equal(idx[-3:].cpu(), ri)

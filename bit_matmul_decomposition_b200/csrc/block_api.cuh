@@ -142,11 +142,11 @@ i8_status run_block_quant(int32_t dtype, blk::QuantArgs a, int64_t Z, bool after
   const int64_t grid = Z * a.row_blocks * a.col_blocks;
   if (!fits_int(grid)) return I8_ERR_INVALID_ARG;
   using Fn = void (*)(blk::QuantArgs);
-  const Fn fns[10] = {blk::block_quant_kernel<false, false, false, 8>, blk::block_quant_kernel<false, false, true, 8>,
-                      blk::block_quant_kernel<false, true, false, 8>, blk::block_quant_kernel<false, true, true, 8>,
-                      blk::block_quant_kernel<true, false, false, 8>, blk::block_quant_kernel<true, false, true, 8>,
-                      blk::block_quant_kernel<true, true, false, 8>, blk::block_quant_kernel<true, true, true, 8>,
-                      blk::block_quant_kernel<false, true, false, 2>, blk::block_quant_kernel<true, true, false, 2>};
+  const Fn fns[10] = {blk::block_quant_kernel<false, false, false, 4>, blk::block_quant_kernel<false, false, true, 4>,
+                      blk::block_quant_kernel<false, true, false, 4>, blk::block_quant_kernel<false, true, true, 4>,
+                      blk::block_quant_kernel<true, false, false, 4>, blk::block_quant_kernel<true, false, true, 4>,
+                      blk::block_quant_kernel<true, true, false, 4>, blk::block_quant_kernel<true, true, true, 4>,
+                      blk::block_quant_kernel<false, true, false, 1>, blk::block_quant_kernel<true, true, false, 1>};
   const Fn f = fns[thin ? 8 + (bf ? 1 : 0) : (bf ? 4 : 0) + (rows ? 2 : 0) + (tiles ? 1 : 0)];
   if (after) {
     const cudaError_t e = launch_overlapped(f, dim3(static_cast<unsigned>(grid)), dim3(blk::kQuantThreads), 0, s, a);

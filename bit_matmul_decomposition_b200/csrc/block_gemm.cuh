@@ -617,13 +617,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int c = 0; c < 4; ++c) {
           const int c0 = n0 + c * 32;
           if (c0 >= a.Nc) continue;
-          if (kOut == kOutF32) {
+          if constexpr (kOut == kOutF32) {
 #pragma unroll
             for (int w = 0; w < 2; ++w)
               store16_f32(cst, &acc[c * 32 + w * 16], static_cast<float*>(a.C) + static_cast<int64_t>(wrow0) * a.ldc, a.ldc,
                           c0 + w * 16, a.Nc, row_end - wrow0);
-            continue;
-          }
+          } else {
           uint32_t o[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j)
@@ -653,6 +652,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               for (int r = 0; r < rows; ++r)
                 dst[static_cast<int64_t>(r) * a.ldc] = lds_u16(cst + static_cast<uint32_t>(r * 64 + lane * 2));
             __syncwarp();
+          }
           }
         }
       }

@@ -112,14 +112,26 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   }
 }
 
-// PASSES: rows of 16 a thread holds; 8 for tiles, 2 when row codes alone are wanted (four times the
-// CTAs: 2048 x 4096 takes 8.4 us, with 128 rows a CTA 9.4; 333 x 4112 3.3 and 6.3).
+// 16 codes of 16 packed values times `up`
+template <bool kBf16>
+__device__ __forceinline__ uint4 codes16_scaled(const uint4& lo, const uint4& hi, float up) {
+  float f[8];
+  unpack8<kBf16>(lo, f);
+  const uint2 x = codes8_scaled(f, up);
+  unpack8<kBf16>(hi, f);
+  const uint2 y = codes8_scaled(f, up);
+  return make_uint4(x.x, x.y, y.x, y.y);
+}
+
+// Eight lanes hold a row's 128 features, 16 each, and the CTA 32 rows at a time.  PASSES: how many
+// times; 4 for tiles, 1 when row codes alone are wanted (four times the CTAs: 333 x 4112 takes 3.3
+// us, with 128 rows a CTA 6.3).
 template <bool kBf16, bool kRows, bool kTiles, int PASSES>
-__global__ void __launch_bounds__(kQuantThreads, PASSES == 2 ? 6 : kRows && kTiles ? 3 : 4)
+__global__ void __launch_bounds__(kQuantThreads, PASSES == 1 ? 6 : kRows && kTiles ? 3 : 4)
     block_quant_kernel(const QuantArgs a) {
-  static_assert(PASSES == 8 || !kTiles, "a tile has 128 rows");
+  static_assert(PASSES == 4 || !kTiles, "a tile has 128 rows");
   __shared__ float s_max[kQuantThreads / 32];
-  __shared__ float s_sum[16][QB];
+  __shared__ float s_sum[32][QB];
   grid_dep_wait();
   grid_dep_launch();
   if (a.zero != nullptr && blockIdx.x == 0)
@@ -129,44 +141,47 @@ __global__ void __launch_bounds__(kQuantThreads, PASSES == 2 ? 6 : kRows && kTil
   b /= a.col_blocks;
   const int rb = static_cast<int>(b % a.row_blocks);
   const int64_t z = b / a.row_blocks;
-  const int r_in = threadIdx.x >> 4;                 // 16 rows a pass, 16 threads a row
-  const int64_t c0 = static_cast<int64_t>(cb) * QB + (threadIdx.x & 15) * 8;
-  const int64_t row0 = static_cast<int64_t>(rb) * (PASSES * 16) + r_in;
+  const int r_in = threadIdx.x >> 3;                 // 32 rows a pass, 8 threads a row
+  const int lane8 = threadIdx.x & 7;
+  const int64_t c0 = static_cast<int64_t>(cb) * QB + lane8 * 16;
+  const int64_t row0 = static_cast<int64_t>(rb) * (PASSES * 32) + r_in;
   const uint16_t* X = a.X + z * a.R * a.C;
   const bool vec = (a.C & 7) == 0;                   // rows start on 16 bytes
-  uint4 v[PASSES];
+  uint4 v[PASSES][2];
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
-    const int64_t r = row0 + p * 16;
-    v[p] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < a.R) {
-      const uint16_t* src = X + r * a.C + c0;
-      if (vec) {
-        if (c0 < a.C) v[p] = ldg_v4(src);
-      } else {
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
+    const int64_t r = row0 + p * 32;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (c0 + i < a.C) w[i >> 1] |= static_cast<uint32_t>(src[i]) << (16 * (i & 1));
-        v[p] = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int h = 0; h < 2; ++h) {
+      const int64_t c = c0 + 8 * h;
+      v[p][h] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < a.R && c < a.C) {
+        const uint16_t* src = X + r * a.C + c;
+        if (vec) {
+          v[p][h] = ldg_v4(src);
+        } else {
+          uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < a.C) w[i >> 1] |= static_cast<uint32_t>(src[i]) << (16 * (i & 1));
+          v[p][h] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
     }
   }
-  float m[PASSES];                                        // the row's maximum over this thread's 8
+  float m[PASSES];                                   // the row's maximum over this thread's 16
 #pragma unroll
-  for (int p = 0; p < PASSES; ++p) m[p] = absmax8<kBf16>(v[p]);
+  for (int p = 0; p < PASSES; ++p) m[p] = fmaxf(absmax8<kBf16>(v[p][0]), absmax8<kBf16>(v[p][1]));
   if (kRows) {
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
-      const int64_t r = row0 + p * 16;
+      const int64_t r = row0 + p * 32;
       float am = m[p];
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+      for (int o = 4; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
       am = fmaxf(am, kScaleFloor);
       if (r >= a.R) continue;
-      float f[8];
-      unpack8<kBf16>(v[p], f);
-      const uint2 q = codes8_scaled(f, block_up(am));
+      const uint4 q = codes16_scaled<kBf16>(v[p][0], v[p][1], block_up(am));
       const float down = block_down(am);
       const int n = a.dest != nullptr ? a.copies : 1;
       for (int j0 = 0; j0 < n; j0 += 4) {            // four places' loads in flight
@@ -177,8 +192,8 @@ __global__ void __launch_bounds__(kQuantThreads, PASSES == 2 ? 6 : kRows && kTil
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (t[j] < 0) continue;
-          if (c0 < a.qr_pitch) *reinterpret_cast<uint2*>(a.Qr + t[j] * a.qr_pitch + c0) = q;
-          if ((threadIdx.x & 15) == 0) a.Sr[cb * a.rows_out + t[j]] = down;
+          if (c0 < a.qr_pitch) *reinterpret_cast<uint4*>(a.Qr + t[j] * a.qr_pitch + c0) = q;
+          if (lane8 == 0) a.Sr[cb * a.rows_out + t[j]] = down;
         }
       }
     }
@@ -197,33 +212,34 @@ __global__ void __launch_bounds__(kQuantThreads, PASSES == 2 ? 6 : kRows && kTil
     const float up = block_up(am);
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
-      const int64_t r = row0 + p * 16;
+      const int64_t r = row0 + p * 32;
       if (r >= a.R || c0 >= a.qt_pitch) continue;
-      float f[8];
-      unpack8<kBf16>(v[p], f);
-      *reinterpret_cast<uint2*>(a.Qt + (z * a.R + r) * a.qt_pitch + c0) = codes8_scaled(f, up);
+      *reinterpret_cast<uint4*>(a.Qt + (z * a.R + r) * a.qt_pitch + c0) = codes16_scaled<kBf16>(v[p][0], v[p][1], up);
     }
     if (threadIdx.x == 0) a.St[blockIdx.x] = block_down(am);
   }
   if (a.colsum != nullptr) {
-    // column sums in a fixed order: each thread its rows from the top, then the 16 threads of
+    // column sums in a fixed order: each thread its rows from the top, then the 32 threads of
     // a column in turn
-    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      float f[8];
-      unpack8<kBf16>(v[p], f);
+    for (int h = 0; h < 2; ++h) {
+      float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += f[i];
+      for (int p = 0; p < PASSES; ++p) {
+        float f[8];
+        unpack8<kBf16>(v[p][h], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += f[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s_sum[r_in][lane8 * 16 + 8 * h + i] = sum[i];
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s_sum[r_in][(threadIdx.x & 15) * 8 + i] = sum[i];
     __syncthreads();
     const int64_t c = static_cast<int64_t>(cb) * QB + threadIdx.x;
     if (threadIdx.x < QB && c < a.C) {
       float t = s_sum[0][threadIdx.x];
 #pragma unroll
-      for (int i = 1; i < 16; ++i) t += s_sum[i][threadIdx.x];
+      for (int i = 1; i < 32; ++i) t += s_sum[i][threadIdx.x];
       a.colsum[static_cast<int64_t>(rb) * a.C + c] = t;
     }
   }

@@ -18,7 +18,7 @@
 // A sum of 128 e4m3 products and the fp32 sum over the blocks are the only accumulations.
 //
 // Design (sm_100a): persistent clusters of two CTAs, 256 x 256 output tiles,
-// tcgen05.mma.cta_group::2 kind::f8f6f4 (M = 256, N = 256, K = 32), a ring of six 32 KB stages
+// tcgen05.mma.cta_group::2 kind::f8f6f4 (M = 256, N = 256, K = 32), a ring of four 32 KB stages
 // filled by TMA (no multicast).  Warps: 0 loads A and B and arms the leader's barrier,
 // 1 lays out the groups' tiles, allocates TMEM and (leader lane 0) issues the MMAs, 3 holds the
 // products of the scales ready in shared memory, 4..11 are the
@@ -46,7 +46,7 @@ namespace blk {
 
 constexpr int TM = 256, TN = 256, HM = 128, HN = 128;
 constexpr int BK = 128;                       // reduction terms (bytes) per stage = one block
-constexpr int STAGES = 6;
+constexpr int STAGES = 4;
 constexpr int A_BYTES = HM * BK;
 constexpr int STAGE_BYTES = A_BYTES + HN * BK;
 constexpr int THREADS = 384;
@@ -56,7 +56,8 @@ constexpr int REGS_NEEDED = (128 * REGS_LOW + 256 * REGS_EPI + THREADS - 1) / TH
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int GROUP_M = 16;                   // m-tiles per raster group
 constexpr int MAX_GROUPS = 512;
-constexpr int CST_BYTES = 8 * 32 * 64;        // output staging: a 32 x 32 16-bit block a warp
+constexpr int CST_WARP = 4 * 32 * 64;         // output staging of a warp: 32 rows x 128 16-bit columns
+constexpr int CST_BYTES = 8 * CST_WARP;
 constexpr int AUX_BYTES = 2 * 2 * 128 * 4;    // bias of the tile's columns, or row maxima
 constexpr int PRE_BYTES = 2064;               // m-tiles before each group
 constexpr int SLOTS = 8;                      // blocks whose scales are held ready
@@ -83,7 +84,7 @@ struct GemmArgs {
   const uint16_t* bias;         // [Nc] in the output's type, or NULL
   void* C;
   int64_t ldc;
-  bool c_tma;
+  bool c_tma;                   // 16-bit output whose rows start on 16 bytes: written by TMA
   // gated form: codes [M][h_pitch] and scales [ceil(Nc/128)][M] of h; g and u in fp32,
   // [M][2][Nc], when GU is not NULL.  Nc = hidden features.
   uint8_t* H;
@@ -183,24 +184,35 @@ __device__ __forceinline__ float fast_sigmoid(float g) {
   return __fdividef(1.0f, 1.0f + e);
 }
 
-// 16 fp32 columns (a thread its row's) of a warp's 32 rows through 2 KB of shared memory, so that
-// four lanes write 64 bytes of one row; written by themselves, a thread's 16 bytes lie a row apart
-// from the next thread's.  rows: how many of the 32 exist; columns from n on (a multiple of 4) do not.
-__device__ __forceinline__ void store16_f32(uint32_t stage, const float* v, float* base, int64_t ld, int col, int n, int rows) {
+// 64 bytes a thread (16 fp32 or 32 16-bit columns of its row) of a warp's 32 rows through 2 KB of
+// shared memory, so that four lanes write 64 bytes of one row; written by themselves, a thread's 16
+// bytes lie a row apart from the next thread's.  base: row 0, first column; of a row's 64 bytes the
+// first `valid` exist (a multiple of 16, or none), of the 32 rows the first `rows`.
+__device__ __forceinline__ void store_rows(uint32_t stage, const uint32_t (&o)[16], void* base, int64_t ld_bytes, int valid,
+                                           int rows) {
   const int lane = lane_id();
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    gemm::sts_v4(stage + static_cast<uint32_t>(lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)), __float_as_uint(v[4 * j]),
-                 __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+    gemm::sts_v4(stage + static_cast<uint32_t>(lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
   __syncwarp();
-  const int j = lane & 3, c = col + 4 * j;
+  const int j = lane & 3;
+  uint4 x[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = i * 8 + (lane >> 2);
-    const uint4 x = lds_v4(stage + static_cast<uint32_t>(r * 64 + ((j ^ ((r >> 1) & 3)) << 4)));
-    if (r < rows && c < n) *reinterpret_cast<uint4*>(base + static_cast<int64_t>(r) * ld + c) = x;
+    x[i] = lds_v4(stage + static_cast<uint32_t>(r * 64 + ((j ^ ((r >> 1) & 3)) << 4)));
   }
+  uint8_t* dst = static_cast<uint8_t*>(base) + (lane >> 2) * ld_bytes + 16 * j;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i * 8 + (lane >> 2) < rows && 16 * j < valid) *reinterpret_cast<uint4*>(dst + i * 8 * ld_bytes) = x[i];
+}
+__device__ __forceinline__ void store16_f32(uint32_t stage, const float* v, float* base, int64_t ld, int col, int n, int rows) {
+  uint32_t o[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(v[j]);
+  store_rows(stage, o, base + col, ld * 4, (n - col) * 4, rows);
 }
 
 // position of tile t of a group of m_tiles x n_tiles: GROUP_M m-tiles, then the next n-tile
@@ -510,7 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int half = (warp - EPI_WARP0) >> 2;       // which 128 columns
     const int et = threadIdx.x - EPI_WARP0 * 32;    // 0..255
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * HN);
-    const uint32_t cst = cstage + static_cast<uint32_t>((warp - EPI_WARP0) * 2048);
+    const uint32_t cst = cstage + static_cast<uint32_t>((warp - EPI_WARP0) * CST_WARP);
     const uint32_t empty_leader0 = gemm::map_to_rank(smem_u32(&bars->tmem_empty[0]), 0);
     uint32_t n = 0;
     int s = 0;                                      // the block's ring stage, as the issuer's
@@ -623,41 +635,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               store16_f32(cst, &acc[c * 32 + w * 16], static_cast<float*>(a.C) + static_cast<int64_t>(wrow0) * a.ldc, a.ldc,
                           c0 + w * 16, a.Nc, row_end - wrow0);
           } else {
-          uint32_t o[16];
+            uint32_t o[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            o[j] = pack2<kOut == kOutBf16>(acc[c * 32 + 2 * j] + bs[c * 32 + 2 * j], acc[c * 32 + 2 * j + 1] + bs[c * 32 + 2 * j + 1]);
-          // 32 rows x 32 columns through shared memory.  (In the 64-byte swizzle, which spares the
-          // stores their bank conflicts, the TMA stores made 2048 x 12288 x 49152 take 1.14 ms
-          // instead of 1.03.)
-          if (a.c_tma && lane == 0) bulk_wait_read_0();
-          __syncwarp();
+            for (int j = 0; j < 16; ++j)
+              o[j] = pack2<kOut == kOutBf16>(acc[c * 32 + 2 * j] + bs[c * 32 + 2 * j], acc[c * 32 + 2 * j + 1] + bs[c * 32 + 2 * j + 1]);
+            if (a.c_tma) {
+              // The warp's 32 x 128 columns wait in shared memory, four TMA stores of 32 x 32 (clipped by
+              // the map) take them out while the next tile runs.  Stores that the warp waits for go at
+              // the rate of all the SMs' tiles at once, 3500 cycles a tile.
+              const uint32_t box = cst + static_cast<uint32_t>(c * 2048);
+              if (c == 0) {
+                if (lane == 0) bulk_wait_read_0();    // the last tile's have left
+                __syncwarp();
+              }
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            gemm::sts_v4(cst + static_cast<uint32_t>(lane * 64 + j * 16), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-          if (a.c_tma) {
-            gemm::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {                        // clipped by the map
-              gemm::tma_store_2d(&tmC, cst, c0, wrow0);
-              gemm::bulk_commit();
-            }
-          } else {
-            // rows that TMA cannot address (an odd number of columns): the warp writes row by row
-            __syncwarp();
-            uint16_t* dst = static_cast<uint16_t*>(a.C) + static_cast<int64_t>(wrow0) * a.ldc + c0 + lane;
-            const int rows = min(32, row_end - wrow0);
-            if (c0 + lane < a.Nc)
+              for (int j = 0; j < 4; ++j)
+                gemm::sts_v4(box + static_cast<uint32_t>(lane * 64 + j * 16), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+              gemm::fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                gemm::tma_store_2d(&tmC, box, c0, wrow0);
+                gemm::bulk_commit();
+              }
+            } else {
+              // rows that do not start on 16 bytes: the warp writes them one by one, a column a lane
+              uint16_t* dst = static_cast<uint16_t*>(a.C) + static_cast<int64_t>(wrow0) * a.ldc + c0;
+              const int rows = min(32, row_end - wrow0);
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                gemm::sts_v4(cst + static_cast<uint32_t>(lane * 64 + j * 16), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+              __syncwarp();
+              if (c0 + lane < a.Nc)
 #pragma unroll 8
-              for (int r = 0; r < rows; ++r)
-                dst[static_cast<int64_t>(r) * a.ldc] = lds_u16(cst + static_cast<uint32_t>(r * 64 + lane * 2));
-            __syncwarp();
-          }
+                for (int r = 0; r < rows; ++r)
+                  dst[static_cast<int64_t>(r) * a.ldc + lane] = lds_u16(cst + static_cast<uint32_t>(r * 64 + lane * 2));
+            }
           }
         }
       }
     }
-    if (lane == 0) gemm::bulk_wait_all();
+    if (lane == 0) gemm::bulk_wait_all();           // the stores are complete before the CTA ends
   }
 
   tc_fence_before();

@@ -8,8 +8,8 @@ tile, value = code * scale) is that of checkpoints stored in it: ``LinearBlockFp
 takes them as they are.
 
 Activations and bias are fp16 or bf16; the output has their type.  Any number of tokens runs in
-the library's kernels (i8_block_linear_forward): up to 128 tokens stream the weight once, more
-take the tensor-core tiles.
+the library's kernels (i8_block_linear_forward): few tokens stream the weight once, more take the
+tensor-core tiles.
 
 Gradients pass straight through the quantisation, in the same 8-bit products
 (i8_block_linear_backward): dx = q(dy) W' with dy in blocks of 128 per token, and for a layer

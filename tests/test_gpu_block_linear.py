@@ -411,3 +411,24 @@ def test_activations_and_gradients_of_more_than_2_31_elements():
     ref = gv @ wv
     R.check(x.grad[-5:], ref, R.product_bound(gv, wv.T, torch.bfloat16, ref, N))
     assert torch.isfinite(w.grad).all()
+
+
+# ------------------------------------------------------------------ wide layers, few tokens
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("T,K,N", [(17, 144, 20737), (32, 1040, 20600), (33, 16, 20501), (64, 400, 20483), (65, 256, 20600)])
+def test_wide_layers(T, K, N, dtype):
+    """More than 80 tiles of 256 outputs: up to 64 tokens stream the weight."""
+    x, codes, scales, b, ref, bound = _forward_case(T, K, N, dtype, N % 2 == 1)
+    ws = torch.full((abi.i8_block_linear_workspace_size(T, N, K),), 255, dtype=torch.uint8, device=DEV)
+    big = torch.full(((T + 2) * N + 16,), 7.0, dtype=dtype, device=DEV)
+    y = big[8:8 + T * N].view(T, N)
+    abi.i8_block_linear_forward(x, codes, scales, b, y, ws)
+    first = y.clone()
+    R.check(first, ref, bound)
+    abi.i8_block_linear_forward(x, codes, scales, b, y, ws)
+    assert torch.equal(first, y) and (big[:8] == 7).all() and (big[8 + T * N:] == 7).all()
+    x[T - 2, K - 1] = float("nan")
+    z = B.linear_block_fp8(x, codes, scales, b)
+    assert torch.isnan(z[T - 2]).all()
+    keep = [t for t in range(T) if t != T - 2]
+    assert torch.equal(z[keep], first[keep])

@@ -307,3 +307,19 @@ def test_gradients_against_differences():
         h = g * torch.sigmoid(g) * u
         terms = (R.rows_value(dy)[t] @ W2[e]) * h
         assert abs(float(wd.grad[t, j]) - slope) <= 2.0 ** -4 * float(terms.abs().sum()) + 1e-6
+
+
+def test_many_rows_of_one_expert_among_many_experts():
+    """Few rows an expert on average, so the weights stream; one expert has several row tiles."""
+    x, w13, w2, idx, w, dy = _case(70, 24, 1, 144, 272, torch.bfloat16, none=0.0)
+    idx[:, 0] = 17
+    idx[::9, 0] = 23
+    codes, W1, W3, W2 = _codes(w13, w2)
+    y, dx, dw = R.experts(x, idx, w, W1, W3, W2, dy)
+    by, bx, bw = _bounds(x, idx, w, W1, W3, W2, dy, y, dx, dw, torch.bfloat16)
+    xd, wd = x.to(DEV).requires_grad_(True), w.to(DEV).requires_grad_(True)
+    out = X.experts_block_fp8(xd, idx.to(DEV), wd, *codes)
+    out.backward(dy.to(DEV))
+    R.check(out, y, by)
+    R.check(xd.grad, dx, bx)
+    R.check(wd.grad, dw, bw)

@@ -164,3 +164,19 @@ def test_more_than_2_31_logits():
     assert torch.equal(w[-100:], w[:100]) and torch.equal(idx[-100:], idx[:100])
     rw, ri, _ = R.route(x[-3:].cpu(), 4, None, "sigmoid", 1, 1, True, 1.0)
     assert torch.equal(idx[-3:].cpu(), ri)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_logits_far_out_take_the_exact_scores(score):
+    """Saturated sigmoids and scores that underflow: equal scores, so the lower index."""
+    x = torch.full((4, 70), -3.0)
+    x[0, 60], x[0, 10], x[0, 33] = 50.0, 40.0, 45.0        # sigmoid: all 1 in 64 bits
+    x[1] = -1000.0
+    x[1, 50], x[1, 3] = 0.0, -900.0                        # softmax: 0 but for one; sigmoid 0
+    x[2, :] = torch.arange(70) * 0.1
+    x[3, 40:] = -math.inf
+    for groups, top in ((1, 1), (7, 3)):
+        w, idx = route_experts(x.to(DEV), 5, score=score, n_groups=groups, top_groups=top)
+        rw, ri, _ = R.route(x, 5, None, score, groups, top, True, 1.0)
+        assert torch.equal(idx.cpu(), ri)
+        R.check(w, rw, _weights_bound(rw, 1.0))

@@ -37,7 +37,6 @@
 #pragma once
 
 #include "block_quant.cuh"
-#include "bwd.cuh"
 #include "common.cuh"
 #include "gemm.cuh"
 

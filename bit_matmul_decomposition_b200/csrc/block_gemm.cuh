@@ -168,20 +168,9 @@ __device__ __forceinline__ void bulk_wait_read_0() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
-// sigmoid(g) for silu(g) = g * sigmoid(g).  exp(-g) = 2^hi * 2^lo with hi + lo = -g * log2(e) to about 2^-47 relative, so
-// the result is within a few units in the last place of fp32.  For g below about -88, exp(-g)
-// overflows to infinity and g / inf = -0: the limit.  g = -inf would be 0 * inf and gives NaN.
-__device__ __forceinline__ float fast_sigmoid(float g) {
-  const float c1 = 1.4426950216293335f, c2 = 1.9259629911266175e-8f;   // log2(e) = c1 + c2
-  const float hi = -g * c1;
-  const float lo = fmaf(-g, c1, -hi) - g * c2;
-  float e;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(hi));
-  e = fmaf(e, lo * 0.6931471805599453f, e);
-  // hi beyond the exponent range: e is inf (or 0); lo may then be NaN or tiny, so pin the limits
-  e = hi > 128.0f ? __int_as_float(0x7f800000) : e;
-  return __fdividef(1.0f, 1.0f + e);
-}
+// sigmoid(g) for silu(g) = g * sigmoid(g), within a few units in the last place of fp32.  For g
+// below about -88, exp(-g) is infinite and the sigmoid 0: g * 0 = -0, the limit.
+__device__ __forceinline__ float fast_sigmoid(float g) { return __fdividef(1.0f, 1.0f + expf(-g)); }
 
 // 64 bytes a thread (16 fp32 or 32 16-bit columns of its row) of a warp's 32 rows through 2 KB of
 // shared memory, so that four lanes write 64 bytes of one row; written by themselves, a thread's 16

@@ -13,7 +13,8 @@ tensor-core tiles.
 
 Gradients pass straight through the quantisation, in the same 8-bit products
 (i8_block_linear_backward): dx = q(dy) W' with dy in blocks of 128 per token, and for a layer
-that trains its 16-bit weight dW = t(dy)^T t(x) in 128 x 128 tiles, db = sum(dy).
+that trains its 16-bit weight dW = t(dy)^T t(x) in 128 x 128 tiles, db = sum(dy).  There is no
+forward-mode derivative: a dual tensor is refused.
 """
 from __future__ import annotations
 
@@ -21,6 +22,7 @@ import contextlib
 from typing import Iterable, Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import abi
 
@@ -42,6 +44,15 @@ def _dense(t: torch.Tensor) -> torch.Tensor:
     if not t.is_contiguous():
         t = t.contiguous()
     return t.clone() if t.data_ptr() % 16 else t
+
+
+def _no_tangent(*tensors):
+    """Refuses forward-mode dual tensors: a library call fills a fresh buffer, which would have
+    no tangent, and so a derivative of zero."""
+    for t in tensors:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError("no forward-mode derivative: the block-scaled layers, routing "
+                                      "and experts have gradients (reverse mode) alone")
 
 
 def _check_input(x: torch.Tensor, K: int, device: torch.device, name: str = "input"):
@@ -136,6 +147,7 @@ def linear_block_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     if codes.dim() != 2:
         raise ValueError("codes: a 2-D tensor is required")
     _check_input(x, codes.shape[1], codes.device)
+    _no_tangent(x, scales, bias)
     x2 = _dense(x if x.dim() == 2 else x.reshape(-1, codes.shape[1]))
     if torch.is_grad_enabled() and (x2.requires_grad or (bias is not None and bias.requires_grad)):
         y = _BlockLinearFn.apply(x2, codes, scales, bias)
@@ -153,6 +165,7 @@ def linear_block_fp8_train(x: torch.Tensor, weight: torch.Tensor,
     _check_input(x, weight.shape[1], weight.device)
     if weight.dtype != x.dtype:
         raise TypeError("weight is %s, input %s: one type is required" % (weight.dtype, x.dtype))
+    _no_tangent(x, weight, bias)
     x2 = _dense(x if x.dim() == 2 else x.reshape(-1, weight.shape[1]))
     y = _BlockLinearTrainFn.apply(x2, weight, bias)
     return y if x.dim() == 2 else y.view(*x.shape[:-1], weight.shape[0])

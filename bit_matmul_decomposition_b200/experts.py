@@ -7,7 +7,7 @@ three products are those of ``LinearBlockFp8``, and adds the results.  ``RoutedE
 layer made of both.
 
 The experts are frozen codes, as ``LinearBlockFp8`` without 16-bit weights: gradients are those
-of the input and of the routing weights (and through them of the router).
+of the input and of the routing weights (and through them of the router), in reverse mode alone.
 """
 from __future__ import annotations
 
@@ -16,7 +16,7 @@ from typing import Iterable, Optional, Tuple
 import torch
 
 from . import abi
-from .block import DTYPES, _check_input, _dense, _on, quantize_weight_blocks
+from .block import DTYPES, _check_input, _dense, _no_tangent, _on, quantize_weight_blocks
 
 
 def _route(logits, balance, score, n_groups, top_groups, k, renormalize, scale):
@@ -61,6 +61,7 @@ def route_experts(logits: torch.Tensor, top_k: int, balance: Optional[torch.Tens
     """
     if score not in abi.SCORES:
         raise ValueError("score must be 'softmax' or 'sigmoid'")
+    _no_tangent(logits, balance)
     if logits.dim() < 1 or not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor [..., E]")
     E = logits.shape[-1]
@@ -139,6 +140,7 @@ def experts_block_fp8(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor,
         raise ValueError("CB13: [E, 2, I, K] codes are required")
     K = CB13.shape[3]
     _check_input(x, K, CB13.device)
+    _no_tangent(x, weights, S13, S2)
     for name, t, dtype in (("idx", idx, torch.int32), ("weights", weights, torch.float32)):
         if t.dtype != dtype:
             raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))

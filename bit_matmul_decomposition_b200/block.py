@@ -14,7 +14,8 @@ tensor-core tiles.
 Gradients pass straight through the quantisation, in the same 8-bit products
 (i8_block_linear_backward): dx = q(dy) W' with dy in blocks of 128 per token, and for a layer
 that trains its 16-bit weight dW = t(dy)^T t(x) in 128 x 128 tiles, db = sum(dy).  There is no
-forward-mode derivative: a dual tensor is refused.
+forward-mode derivative (a dual tensor is refused) and no second one (create_graph gives the same
+gradients, and differentiating them again raises).
 """
 from __future__ import annotations
 
@@ -53,6 +54,37 @@ def _no_tangent(*tensors):
         if t is not None and forward_ad.unpack_dual(t).tangent is not None:
             raise NotImplementedError("no forward-mode derivative: the block-scaled layers, routing "
                                       "and experts have gradients (reverse mode) alone")
+
+
+class _FirstOrder(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, grad, *depends):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise NotImplementedError("no second derivative: the block-scaled layers, routing and "
+                                  "experts have first-order gradients alone")
+
+
+def _first_order(grad, *depends):
+    """A gradient on its way out of a backward that the library computed.  Under create_graph it
+    is tied to the tensors of the graph that it depends on, so that differentiating it again
+    raises; without the tie its terms would be missing from the sum and no error seen.
+    (torch.autograd.function.once_differentiable ties it to the gradients that came in alone: a
+    constant one, as sum() gives, leaves nothing to raise.)"""
+    if grad is None or not torch.is_grad_enabled():
+        return grad
+    depends = [t for t in depends if t is not None and t.requires_grad]
+    return _FirstOrder.apply(grad, *depends) if depends else grad
+
+
+def _tie(t):
+    """For a tensor that a backward does not read: what `_first_order` needs of it.  A leaf itself,
+    or an empty tensor with the history of `t` but none of its memory."""
+    if not t.requires_grad or t.is_leaf:
+        return t if t.requires_grad else None
+    return torch.slice_copy(t, 0, 0, 0)
 
 
 def _check_input(x: torch.Tensor, K: int, device: torch.device, name: str = "input"):
@@ -122,22 +154,26 @@ class _BlockLinearFn(torch.autograd.Function):
         codes, scales = ctx.saved_tensors
         gx, _, gb = _backward(gy, None, codes, scales, codes.shape[1], ctx.needs_input_grad[0],
                               False, ctx.needs_input_grad[3], ctx.dtype)
-        return gx, None, None, gb
+        return _first_order(gx, gy), None, None, _first_order(gb, gy)
 
 
 class _BlockLinearTrainFn(torch.autograd.Function):
     """A 16-bit weight, quantised by every forward: gradients of input, weight and bias."""
 
     @staticmethod
-    def forward(ctx, x2, weight, bias):
+    def forward(ctx, x2, weight, bias, tie):
         codes, scales = quantize_weight_blocks(weight)
         ctx.save_for_backward(x2, codes, scales)
+        ctx.tie = tie[0]
         return _forward(x2, codes, scales, bias)
 
     @staticmethod
     def backward(ctx, gy):
         x2, codes, scales = ctx.saved_tensors
-        return _backward(gy, x2, codes, scales, codes.shape[1], *ctx.needs_input_grad, x2.dtype)
+        gx, gw, gb = _backward(gy, x2, codes, scales, codes.shape[1], *ctx.needs_input_grad[:3],
+                               x2.dtype)
+        return (_first_order(gx, gy, ctx.tie), _first_order(gw, gy, x2), _first_order(gb, gy),
+                None)
 
 
 def linear_block_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
@@ -167,7 +203,7 @@ def linear_block_fp8_train(x: torch.Tensor, weight: torch.Tensor,
         raise TypeError("weight is %s, input %s: one type is required" % (weight.dtype, x.dtype))
     _no_tangent(x, weight, bias)
     x2 = _dense(x if x.dim() == 2 else x.reshape(-1, weight.shape[1]))
-    y = _BlockLinearTrainFn.apply(x2, weight, bias)
+    y = _BlockLinearTrainFn.apply(x2, weight, bias, (_tie(weight),))
     return y if x.dim() == 2 else y.view(*x.shape[:-1], weight.shape[0])
 
 

@@ -7,7 +7,7 @@ three products are those of ``LinearBlockFp8``, and adds the results.  ``RoutedE
 layer made of both.
 
 The experts are frozen codes, as ``LinearBlockFp8`` without 16-bit weights: gradients are those
-of the input and of the routing weights (and through them of the router), in reverse mode alone.
+of the input and of the routing weights (and through them of the router), in reverse mode and of the first order alone.
 """
 from __future__ import annotations
 
@@ -16,7 +16,8 @@ from typing import Iterable, Optional, Tuple
 import torch
 
 from . import abi
-from .block import DTYPES, _check_input, _dense, _no_tangent, _on, quantize_weight_blocks
+from .block import (DTYPES, _check_input, _dense, _first_order, _no_tangent, _on, _tie,
+                    quantize_weight_blocks)
 
 
 def _route(logits, balance, score, n_groups, top_groups, k, renormalize, scale):
@@ -46,7 +47,7 @@ class _RouteFn(torch.autograd.Function):
         if logits.shape[0] > 0:
             with _on(logits.device):
                 abi.i8_route_experts_backward(logits, *ctx.how, idx, _dense(gw), gl)
-        return (gl,) + (None,) * 7
+        return (_first_order(gl, gw, logits),) + (None,) * 7
 
 
 def route_experts(logits: torch.Tensor, top_k: int, balance: Optional[torch.Tensor] = None, *,
@@ -105,10 +106,10 @@ def _forward(x2, idx, w, CB13, S13, CB2, S2, keep):
 
 class _ExpertsFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x2, w, idx, CB13, S13, CB2, S2):
+    def forward(ctx, x2, w, idx, CB13, S13, CB2, S2, tie):
         y, gu = _forward(x2, idx, w, CB13, S13, CB2, S2, True)
         ctx.save_for_backward(w, idx, CB13, S13, CB2, S2, gu)
-        ctx.dtype = x2.dtype
+        ctx.dtype, ctx.tie = x2.dtype, tie[0]
         return y
 
     @staticmethod
@@ -123,7 +124,7 @@ class _ExpertsFn(torch.autograd.Function):
                                 dtype=torch.uint8)
             with _on(gy.device):
                 abi.i8_experts_backward(gy, idx, w, CB13, S13, CB2, S2, gu, gx, gw, ws)
-        return gx, gw, None, None, None, None, None
+        return (_first_order(gx, gy, ctx.tie, w), _first_order(gw, gy, ctx.tie)) + (None,) * 6
 
 
 def experts_block_fp8(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor,
@@ -155,7 +156,7 @@ def experts_block_fp8(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor,
         raise ValueError("%d experts, %d a token: at most 512 and 1 to 32" % (CB13.shape[0], k))
     x2, i2, w2 = (_dense(t if t.dim() == 2 else t.reshape(-1, t.shape[-1])) for t in (x, idx, weights))
     if torch.is_grad_enabled() and (x2.requires_grad or w2.requires_grad):
-        y = _ExpertsFn.apply(x2, w2, i2, CB13, S13, CB2, S2)
+        y = _ExpertsFn.apply(x2, w2, i2, CB13, S13, CB2, S2, (_tie(x2),))
     else:
         y, _ = _forward(x2, i2, w2, CB13, S13, CB2, S2, False)
     return y if x.dim() == 2 else y.view(x.shape)

@@ -86,3 +86,69 @@ def test_routing_refuses_tangents(which):
         a[which] = fwAD.make_dual(a[which], torch.ones_like(a[which]))
         with pytest.raises(NotImplementedError, match="forward-mode"):
             experts.route_experts(**a)
+
+
+# ------------------------------------------------------------------ second derivatives
+def _calls():
+    """Name: (call, its differentiable inputs, which inputs' gradients each gradient depends on,
+    besides the gradient of the output)."""
+    x, codes, scales, b = _linear()
+    w = torch.ones((N, K), dtype=H)
+    ex = _experts()
+    logits = torch.ones((T, E))
+    return {
+        "linear": (lambda x, b: block.linear_block_fp8(x, codes, scales, b), (x, b), ((), ())),
+        "train": (block.linear_block_fp8_train, (x, w, b), ((1,), (0,), ())),
+        "route": (lambda v: experts._RouteFn.apply(v, None, "softmax", 1, 1, k, True, 1.0)[0], (logits,), ((0,),)),
+        "experts": (lambda x, w: experts.experts_block_fp8(x, ex[1], w, *ex[3:]), (ex[0], ex[2]), ((0, 1), (0,))),
+    }
+
+
+@pytest.mark.parametrize("leaf", [True, False])
+@pytest.mark.parametrize("name", ["linear", "train", "route", "experts"])
+def test_second_derivatives_are_refused(filled, name, leaf):
+    call, inputs, deps = _calls()[name]
+    for i, needs in enumerate(deps):
+        for other in range(len(inputs)):
+            # the gradient of input i, differentiated again with respect to input `other`; the
+            # loss reaches `other` by a second way, so that a lost term would raise nothing
+            roots = [v.clone().requires_grad_(True) for v in inputs]
+            args = roots if leaf else [v * 1 for v in roots]
+            y = call(*args)
+            first, = torch.autograd.grad(y.float().sum(), args[i], create_graph=True)
+            loss = first.float().square().sum() + sum(v.float().square().sum() for v in roots)
+            if other in needs:
+                with pytest.raises(NotImplementedError, match="second"):
+                    torch.autograd.grad(loss, roots[other])
+            else:                                          # does not depend on it: nothing is lost
+                torch.autograd.grad(loss, roots[other])
+        # through the gradient of the output, on which every gradient depends
+        roots = [v.clone().requires_grad_(True) for v in inputs]
+        y = call(*roots)
+        gy = torch.ones_like(y).requires_grad_(True)
+        first, = torch.autograd.grad(y, roots[i], gy, create_graph=True)
+        with pytest.raises(NotImplementedError, match="second"):
+            torch.autograd.grad(first.float().square().sum() + gy.float().square().sum(), gy)
+
+
+def test_first_derivatives_under_create_graph(filled):
+    """Gradients taken with create_graph are the same, and may be used where nothing is
+    differentiated again."""
+    for name, (call, inputs, _) in _calls().items():
+        roots = [v.clone().requires_grad_(True) for v in inputs]
+        once = torch.autograd.grad(call(*roots).float().sum(), roots)
+        again = torch.autograd.grad(call(*roots).float().sum(), roots, create_graph=True)
+        assert all(torch.equal(a, b) for a, b in zip(once, again)), name
+        call(*roots).float().sum().backward(create_graph=True)
+        assert all(v.grad is not None for v in roots)
+
+
+def test_frozen_inputs_carry_no_second_derivative(filled):
+    """With a constant gradient of the output the frozen layer's dx is a constant."""
+    x, codes, scales, b = _linear()
+    x.requires_grad_(True)
+    gx, = torch.autograd.grad(block.linear_block_fp8(x, codes, scales, b).float().sum(), x, create_graph=True)
+    assert not gx.requires_grad
+    w = torch.ones((N, K), dtype=H)
+    gx, = torch.autograd.grad(block.linear_block_fp8_train(x, w, b).float().sum(), x, create_graph=True)
+    assert not gx.requires_grad

@@ -207,7 +207,30 @@ def linear_block_fp8_train(x: torch.Tensor, weight: torch.Tensor,
     return y if x.dim() == 2 else y.view(*x.shape[:-1], weight.shape[0])
 
 
-class LinearBlockFp8(torch.nn.Module):
+class FixedTypes(torch.nn.Module):
+    """A module some of whose tensors have the one type that the library takes: casts of the
+    model (``.half()``, ``.to(torch.bfloat16)``, ``.double()``) move them, but leave type and values
+    alone.  Cast, the scales would lose bits for good, and fp16 holds few of them at all."""
+
+    FIXED: Tuple[str, ...] = ()                # names of such buffers and parameters
+
+    def _apply(self, fn, recurse=True):
+        if recurse:
+            for child in self.children():
+                child._apply(fn)
+        fixed = [t for t in (getattr(self, name, None) for name in self.FIXED) if t is not None]
+        fixed += [t.grad for t in fixed if t.grad is not None]
+
+        def keep(t):
+            out = fn(t)
+            if out.dtype != t.dtype and any(t is f for f in fixed):
+                return t.detach().to(out.device)
+            return out
+
+        return super()._apply(keep, recurse=False)
+
+
+class LinearBlockFp8(FixedTypes):
     """nn.Linear with a block-scaled e4m3 weight.
 
     Buffers (saved by ``state_dict``): ``CB`` uint8 [out, in] e4m3 codes, ``SCB`` fp32
@@ -215,8 +238,11 @@ class LinearBlockFp8(torch.nn.Module):
     weight and the bias are parameters of type `dtype` instead, quantised by every forward, and
     the layer trains; without, it passes the gradient of its input.
 
-    in_features must be a multiple of 16; out_features may be any number.
+    in_features must be a multiple of 16; out_features may be any number.  A cast of the model
+    changes the type of weight and bias; codes and scales keep theirs.
     """
+
+    FIXED = ("CB", "SCB")
 
     def __init__(self, in_features: int, out_features: int, bias: bool = True, device=None,
                  dtype: torch.dtype = torch.bfloat16, has_16bit_weights: bool = False):

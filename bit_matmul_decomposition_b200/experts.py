@@ -16,8 +16,8 @@ from typing import Iterable, Optional, Tuple
 import torch
 
 from . import abi
-from .block import (DTYPES, _check_input, _dense, _first_order, _no_tangent, _on, _tie,
-                    quantize_weight_blocks)
+from .block import (DTYPES, FixedTypes, _check_input, _dense, _first_order, _no_tangent, _on,
+                    _tie, quantize_weight_blocks)
 
 
 def _route(logits, balance, score, n_groups, top_groups, k, renormalize, scale):
@@ -162,9 +162,12 @@ def experts_block_fp8(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor,
     return y if x.dim() == 2 else y.view(x.shape)
 
 
-class ExpertsBlockFp8(torch.nn.Module):
+class ExpertsBlockFp8(FixedTypes):
     """E gated feed-forward experts of width `hidden` on `features` features, as block-scaled
-    e4m3 codes (buffers ``CB13``, ``S13``, ``CB2``, ``S2``, saved by ``state_dict``)."""
+    e4m3 codes (buffers ``CB13``, ``S13``, ``CB2``, ``S2``, saved by ``state_dict``; casts of the
+    model leave their types alone)."""
+
+    FIXED = ("CB13", "S13", "CB2", "S2")
 
     def __init__(self, num_experts: int, features: int, hidden: int, device=None):
         super().__init__()
@@ -218,11 +221,14 @@ class ExpertsBlockFp8(torch.nn.Module):
                                                            self.hidden)
 
 
-class RoutedExperts(torch.nn.Module):
+class RoutedExperts(FixedTypes):
     """A feed-forward layer of experts: router logits x G^T (fp32), route_experts, the experts.
 
     ``gate``: the router's weight [E, features], a parameter; ``balance``: fp32 [E], a buffer
-    that the user's program moves to even out the load, or absent."""
+    that the user's program moves to even out the load, or absent.  Both stay fp32 when the model
+    is cast."""
+
+    FIXED = ("gate", "balance")
 
     def __init__(self, experts: ExpertsBlockFp8, top_k: int, gate: Optional[torch.Tensor] = None,
                  balance: bool = False, score: str = "softmax", n_groups: int = 1,

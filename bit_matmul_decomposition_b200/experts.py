@@ -11,6 +11,7 @@ of the input and of the routing weights (and through them of the router), in rev
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Iterable, Optional, Tuple
 
 import torch
@@ -248,6 +249,9 @@ class RoutedExperts(FixedTypes):
                             renormalize=renormalize, scale=scale)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        logits = torch.nn.functional.linear(x.float(), self.gate)
+        # near-equal scores decide the choice: no 16-bit product here, under autocast either
+        with torch.autocast(x.device.type, enabled=False) \
+                if torch.is_autocast_enabled(x.device.type) else contextlib.nullcontext():
+            logits = torch.nn.functional.linear(x.float(), self.gate)
         w, idx = route_experts(logits, self.top_k, self.balance, **self.routing)
         return self.experts(x, idx, w)

@@ -67,3 +67,24 @@ def test_moves_still_move():
     assert m[0].experts.S13.dtype == torch.float32
     m = m.half().to_empty(device="cpu")
     assert m[0].experts.S13.dtype == torch.float32 and not m[0].gate.is_meta and m[1].weight.dtype == torch.float16
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_router_logits_stay_fp32_under_autocast(monkeypatch, dtype):
+    seen = {}
+
+    def route(logits, *a, **kw):
+        seen["logits"] = logits
+        return torch.ones((*logits.shape[:-1], 2)), torch.zeros((*logits.shape[:-1], 2), dtype=torch.int32)
+    monkeypatch.setattr(experts, "route_experts", route)
+    monkeypatch.setattr(experts, "experts_block_fp8", lambda x, *a: x)
+    r = _layer("routed")[0]
+    x = torch.randn(5, 144, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    r(x)
+    plain = seen["logits"]
+    with torch.autocast("cpu", dtype=dtype):
+        r(x)
+        assert torch.is_autocast_enabled("cpu")
+    assert seen["logits"].dtype == torch.float32 and torch.equal(seen["logits"], plain)
+    seen["logits"].sum().backward()
+    assert torch.equal(r.gate.grad, x.float().sum(0).expand(3, 144))

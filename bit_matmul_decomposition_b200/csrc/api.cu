@@ -1087,7 +1087,7 @@ i8_status i8_block_quantize_weight(const void* W, int32_t dtype, int64_t Z, int6
 }
 
 size_t i8_block_linear_workspace_size(int64_t T, int64_t N, int64_t K) {
-  if (!shape_ok(T, K) || !fits_int(N)) return 0;
+  if (!product_ok(T, N, K)) return 0;
   return linear_ws(T, N, K).total;
 }
 
@@ -1097,7 +1097,7 @@ i8_status i8_block_linear_forward(const void* X, int32_t dtype, int64_t T, int64
   if (!X || !CB || !SCB || !Y || !workspace || !aligned16(X) || !aligned16(CB) || !aligned16(SCB) ||
       !aligned16(bias) || !aligned16(Y) || !aligned16(workspace))
     return I8_ERR_INVALID_ARG;
-  if (!dtype16(dtype) || !shape_ok(T, K) || !fits_int(N)) return I8_ERR_INVALID_ARG;
+  if (!dtype16(dtype) || !product_ok(T, N, K)) return I8_ERR_INVALID_ARG;
   if (workspace_bytes < linear_ws(T, N, K).total) return I8_ERR_INVALID_ARG;
   DeviceInfo* d;
   i8_status st = device_info(&d);
@@ -1107,7 +1107,7 @@ i8_status i8_block_linear_forward(const void* X, int32_t dtype, int64_t T, int64
 }
 
 size_t i8_block_linear_backward_workspace_size(int64_t T, int64_t N, int64_t K) {
-  if (!shape_ok(T, K) || !fits_int(N)) return 0;
+  if (!product_ok(T, N, K)) return 0;
   return linear_bwd_ws(T, N, K).total;
 }
 
@@ -1120,7 +1120,7 @@ i8_status i8_block_linear_backward(const void* dY, const void* X, int32_t dtype,
   if (dW && !X) return I8_ERR_INVALID_ARG;
   if (!aligned16(X) || !aligned16(CB) || !aligned16(SCB) || !aligned16(dX) || !aligned16(dW) || !aligned16(db))
     return I8_ERR_INVALID_ARG;
-  if (!dtype16(dtype) || !shape_ok(T, K) || !fits_int(N)) return I8_ERR_INVALID_ARG;
+  if (!dtype16(dtype) || !product_ok(T, N, K)) return I8_ERR_INVALID_ARG;
   if (workspace_bytes < linear_bwd_ws(T, N, K).total) return I8_ERR_INVALID_ARG;
   DeviceInfo* d;
   i8_status st = device_info(&d);

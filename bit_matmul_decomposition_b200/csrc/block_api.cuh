@@ -8,6 +8,10 @@ constexpr int kPartGrid = 160;                // CTAs that the workspace of a sp
 bool dtype16(int32_t dt) { return dt == I8_DTYPE_F16 || dt == I8_DTYPE_BF16; }
 bool fits_int(int64_t v) { return v > 0 && v <= 0x7fffffffLL; }
 int64_t blocks128(int64_t n) { return (n + 127) / 128; }
+// Sizes of a product.  The kernels number rows and columns with 32 bits, in tiles of up to 256: the
+// last tile has to end below 2^31.
+bool tiles_ok(int64_t v) { return v > 0 && v <= 0x80000000LL - 256; }
+bool product_ok(int64_t T, int64_t N, int64_t K) { return tiles_ok(T) && tiles_ok(N) && tiles_ok(K) && K % 16 == 0; }
 
 // ------------------------------------------------------------------ kernels' attributes
 using BlockGemmFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, blk::GemmArgs);
@@ -440,8 +444,9 @@ struct ExpertsShape {
 };
 
 bool experts_shape(int64_t T, int64_t K, int64_t I, int64_t E, int64_t k, ExpertsShape* o) {
-  if (!shape_ok(T, K) || !shape_ok(T, I) || E <= 0 || E > moe::MAX_EXPERTS || k <= 0 || k > moe::MAX_CHOICES) return false;
-  if (!fits_int(T * k) || !fits_int(2 * E) || I > 0x3fffffffLL) return false;
+  if (T <= 0 || !product_ok(1, I, K) || I % 16 != 0 || E <= 0 || E > moe::MAX_EXPERTS || k <= 0 || k > moe::MAX_CHOICES)
+    return false;
+  if (T > 0x7fffffffLL || !tiles_ok(T * k) || !fits_int(2 * E) || I > 0x3fffffffLL) return false;
   *o = ExpertsShape{T, K, I, E, k, T * k, blocks128(I) * 128, static_cast<int>(blocks128(K)), static_cast<int>(blocks128(I))};
   return true;
 }

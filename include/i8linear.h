@@ -351,7 +351,8 @@ i8_status i8_igemm_s32(const int8_t* A, int64_t T, int64_t K, const int8_t* B, i
  * NaN, and no others.
  *
  * dtype: the 16-bit type of X, bias, Y and of the gradients, I8_DTYPE_F16 or I8_DTYPE_BF16.
- * Shapes: T, N, K > 0 and K % 16 == 0; N may be any number.  All pointers 16-byte aligned.
+ * Shapes: T, N, K > 0 and K % 16 == 0; N may be any number; the products take T, N and K up to
+ * 2^31 - 256.  All pointers 16-byte aligned.
  *
  * i8_block_quantize_act(X, dtype, T, K, Xq, SX, stream):
  *   Xq [T, K] codes, SX [ceil(K/128), T] scales (block-major: the T scales of a block of
@@ -431,7 +432,8 @@ i8_status i8_route_experts_backward(const void* logits, int32_t dtype, int64_t T
  *   CB13 [E, 2, I, K] codes (W1 then W3), S13 [E, 2, ceil(I/128), ceil(K/128)] scales,
  *   CB2 [E, K, I], S2 [E, ceil(K/128), ceil(I/128)]: i8_block_quantize_weight with Z = 2E and E
  *   GU [T * k, 2, I] fp32 or NULL: g and u, for the backward (in the library's own row order)
- * Shapes: T, K, I > 0, K % 16 == 0, I % 16 == 0, E <= 512, k <= 32 (k may exceed E).
+ * Shapes: T, K, I > 0, K % 16 == 0, I % 16 == 0, E <= 512, k <= 32 (k may exceed E); T * k and
+ * K up to 2^31 - 256, I below 2^30.
  *
  * i8_experts_backward: the experts are frozen; gradients of x and of the weights:
  *   dh = q(dY) W2;  dweights[t,j] = sum_i dh_i h_i;  dX = sum_j ( q(dg) W1 + q(du) W3 ) with

@@ -37,16 +37,12 @@ BlockGemmFn block_gemm_fn(bool amn, bool bmn, int out) {
                              : blk::block_gemm_kernel<true, true, blk::kOutBf16>;
 }
 
-// the streaming product: tiles of 16 tokens form their codes themselves, larger ones take the
-// quantiser's
+// the streaming product: tiles of 16 tokens form their codes themselves, larger ones (of a layer,
+// so with 16-bit outputs) take the quantiser's
 template <int NT>
 SkinnyFn skinny_fn_nt(int out) {
   using namespace skinny;
-  switch (out) {
-    case blk::kOutF16: return block_skinny_kernel<NT, blk::kOutF16, kInCodes>;
-    case blk::kOutBf16: return block_skinny_kernel<NT, blk::kOutBf16, kInCodes>;
-    default: return block_skinny_kernel<NT, blk::kOutF32, kInCodes>;
-  }
+  return out == blk::kOutBf16 ? block_skinny_kernel<NT, blk::kOutBf16, kInCodes> : block_skinny_kernel<NT, blk::kOutF16, kInCodes>;
 }
 
 SkinnyFn skinny_fn(int nt, int out, int in) {
@@ -56,10 +52,7 @@ SkinnyFn skinny_fn(int nt, int out, int in) {
     return out == blk::kOutF32 ? block_skinny_kernel<16, blk::kOutF32, kInF16> : block_skinny_kernel<16, blk::kOutF16, kInF16>;
   if (in == kInBf16)
     return out == blk::kOutF32 ? block_skinny_kernel<16, blk::kOutF32, kInBf16> : block_skinny_kernel<16, blk::kOutBf16, kInBf16>;
-  switch (nt) {
-    case 32: return skinny_fn_nt<32>(out);
-    default: return skinny_fn_nt<64>(out);
-  }
+  return nt == 32 ? skinny_fn_nt<32>(out) : skinny_fn_nt<64>(out);
 }
 
 struct BlockInfo {
@@ -104,7 +97,7 @@ i8_status block_info(const DeviceInfo& d, BlockInfo** out) {
       clusters = clusters == 0 || c < clusters ? c : clusters;
     }
     for (int o = blk::kOutF16; o <= blk::kOutF32; ++o) {
-      for (int nt = 32; nt <= 64; nt *= 2)
+      for (int nt = 32; nt <= 64 && o != blk::kOutF32; nt *= 2)
         if (!cuda_ok(cudaFuncSetAttribute(skinny_fn(nt, o, skinny::kInCodes), smem_attr, static_cast<int>(skinny::smem_bytes(nt))),
                      "cudaFuncSetAttribute(block skinny)"))
           return I8_ERR_CUDA;

@@ -78,7 +78,7 @@ struct Args {
   int groups;
   const int32_t* offsets;       // as in GemmArgs
   int z_per_group;
-  const float* SA;              // [k_blocks][M]
+  const float* SA;              // [k_blocks][M]: the scales of the quantiser's codes
   const float* SB;              // [z][n_per_z][k_blocks]
   const uint16_t* bias;         // [z_cols] in the output's type, or NULL (one z slice)
   void* C;                      // [M][ldc]
@@ -149,6 +149,7 @@ template <int NT, int kOut, int kIn>
 __global__ void __launch_bounds__(threads(kIn), 1)
     block_skinny_kernel(const __grid_constant__ CUtensorMap tmW,
                         const __grid_constant__ CUtensorMap tmX, const Args a) {
+  static_assert(kIn == kInCodes ? NT > 16 && kOut != blk::kOutF32 : NT == 16, "forms that are launched");
   constexpr int STAGES = stages(NT);
   constexpr int SBYTES = stage_bytes(NT);
   constexpr uint32_t TMEM_COLS = NBUF * NT < 32 ? 32 : NBUF * NT;
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(threads(kIn), 1)
     tmem_alloc(smem_u32(&bars->tmem_base), TMEM_COLS);
     tmem_relinquish();
   }
-  const bool grouped = a.offsets != nullptr;
+  const bool grouped = kIn != kInCodes && a.offsets != nullptr;
   if (grouped) {
     grid_dep_wait();
     grid_dep_launch();
@@ -265,9 +266,9 @@ __global__ void __launch_bounds__(threads(kIn), 1)
     if (lane == 0) {
       // ---------------------------------------------------------------- TMA producer
       // One pass over the run.  While the kernel before may still write the tokens' codes
-      // (dense form), the first STAGES units get their weight half only; then the wait, their
+      // (kInCodes), the first STAGES units get their weight half only; then the wait, their
       // token halves, and the rest of the run whole.
-      const int64_t head = grouped || kIn != kInCodes ? 0 : (u1 - u0 < STAGES ? u1 - u0 : STAGES);
+      const int64_t head = kIn != kInCodes ? 0 : (u1 - u0 < STAGES ? u1 - u0 : STAGES);
       auto issue = [&](int64_t u, int s, bool w, bool x, int& row0, int& z, int& nz, int& last_tile) {
         const int tile = static_cast<int>(u / KB);
         const int kb = static_cast<int>(u - static_cast<int64_t>(tile) * KB);
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(threads(kIn), 1)
   } else if (warp == 6) {
     // ------------------------------------------------------------------ scales
     // SA * SB of each unit's tokens, AHEAD units loaded together
-    if (!grouped) grid_dep_wait();
+    grid_dep_wait();
     constexpr int SL = (NT + 31) / 32;              // tokens of a lane
     constexpr int AHEAD = SL > 2 ? 4 : 8;
     uint32_t n = 0;

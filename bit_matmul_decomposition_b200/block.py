@@ -52,8 +52,8 @@ def _no_tangent(*tensors):
     no tangent, and so a derivative of zero."""
     for t in tensors:
         if t is not None and forward_ad.unpack_dual(t).tangent is not None:
-            raise NotImplementedError("no forward-mode derivative: the block-scaled layers, routing "
-                                      "and experts have gradients (reverse mode) alone")
+            raise NotImplementedError("no forward-mode derivative: the library's layers have "
+                                      "gradients (reverse mode) alone")
 
 
 class _FirstOrder(torch.autograd.Function):
@@ -63,8 +63,8 @@ class _FirstOrder(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, _):
-        raise NotImplementedError("no second derivative: the block-scaled layers, routing and "
-                                  "experts have first-order gradients alone")
+        raise NotImplementedError("no second derivative: the library's layers have first-order "
+                                  "gradients alone")
 
 
 def _first_order(grad, *depends):

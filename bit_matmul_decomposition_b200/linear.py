@@ -17,7 +17,8 @@ still passes dx = dy W' back (W' = CB * SCB / 127, the weight it computes with),
 before it can train.  Forward and backward run in the library's CUDA kernels: the two
 backward products on the tcgen05 tensor cores (i8_linear_backward_input / _weight), the
 bias gradient and W' in HBM-bound passes (i8_bias_grad, i8_dequantize_weight).  The
-backward needs out_features % 8 == 0 (the row pitch of dy must suit TMA).
+backward needs out_features % 8 == 0 (the row pitch of dy must suit TMA).  There is no
+forward-mode derivative: a dual tensor is refused.
 
 Serving with systematic outliers (the blog's observation that the same few feature
 dimensions carry the outliers call after call): ``outlier_cache_cols > 0`` keeps the
@@ -35,6 +36,7 @@ from typing import Dict, Iterable, Optional
 import torch
 
 from . import abi
+from .block import _no_tangent
 
 
 class _Int8LinearFn(torch.autograd.Function):
@@ -259,6 +261,7 @@ class Linear8bitLt(torch.nn.Module):
                              % (x.shape[-1], self.in_features))
         if x.device != self.CB.device:
             raise ValueError("input on %s, layer on %s" % (x.device, self.CB.device))
+        _no_tangent(x, self.bias, self.weight if self.has_fp16_weights else None)
         lead = x.shape[:-1]
         x2 = x.reshape(-1, self.in_features).contiguous()
         if self.has_fp16_weights:

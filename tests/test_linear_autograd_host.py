@@ -1,0 +1,46 @@
+"""Linear8bitLt on the CPU: derivatives that it does not have are refused, and casts of a model leave
+its codes and scales alone.  The library's calls are replaced by ones that only make the buffers."""
+import contextlib
+
+import pytest
+import torch
+import torch.autograd.forward_ad as fwAD
+
+from bit_matmul_decomposition_b200 import abi, linear
+
+T, K, N = 4, 32, 16
+H = torch.float16
+
+
+def _layer(monkeypatch, fp16_weights):
+    m = linear.Linear8bitLt(K, N, has_fp16_weights=fp16_weights)
+    monkeypatch.setattr(m, "_forward_kernel", lambda x: torch.ones((x.shape[0], N), dtype=H))
+    monkeypatch.setattr(m, "_quantize", lambda w: None)
+    monkeypatch.setattr(m, "dequantized_weight", lambda: torch.ones((N, K), dtype=H))
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    for name, at in (("i8_linear_backward_input", 2), ("i8_linear_backward_weight", 2), ("i8_bias_grad", 1)):
+        monkeypatch.setattr(abi, name, lambda *a, at=at: a[at].fill_(1))
+    return m
+
+
+@pytest.mark.parametrize("fp16_weights", [True, False])
+@pytest.mark.parametrize("grad", [True, False])
+def test_tangents_are_refused(monkeypatch, fp16_weights, grad):
+    m = _layer(monkeypatch, fp16_weights)
+    x = torch.ones((T, K), dtype=H)
+    with fwAD.dual_level(), torch.set_grad_enabled(grad):
+        m(x)
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            m(fwAD.make_dual(x, torch.ones_like(x)))
+
+
+@pytest.mark.parametrize("which", ["weight", "bias"])
+def test_tangents_of_parameters_are_refused(monkeypatch, which):
+    m = _layer(monkeypatch, True)
+    x = torch.ones((T, K), dtype=H)
+    with fwAD.dual_level():
+        p = getattr(m, which).detach().clone()
+        delattr(m, which)
+        setattr(m, which, fwAD.make_dual(p, torch.ones_like(p)))
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            m(x)

@@ -18,7 +18,8 @@ before it can train.  Forward and backward run in the library's CUDA kernels: th
 backward products on the tcgen05 tensor cores (i8_linear_backward_input / _weight), the
 bias gradient and W' in HBM-bound passes (i8_bias_grad, i8_dequantize_weight).  The
 backward needs out_features % 8 == 0 (the row pitch of dy must suit TMA).  There is no
-forward-mode derivative: a dual tensor is refused.
+forward-mode derivative (a dual tensor is refused) and no second one (gradients taken with
+create_graph raise when they are differentiated again).
 
 Serving with systematic outliers (the blog's observation that the same few feature
 dimensions carry the outliers call after call): ``outlier_cache_cols > 0`` keeps the
@@ -36,7 +37,7 @@ from typing import Dict, Iterable, Optional
 import torch
 
 from . import abi
-from .block import _no_tangent
+from .block import _first_order, _no_tangent
 
 
 class _Int8LinearFn(torch.autograd.Function):
@@ -82,7 +83,8 @@ class _Int8LinearFn(torch.autograd.Function):
             if want_b:
                 gb = torch.empty((N,), dtype=torch.float16, device=dev)
                 abi.i8_bias_grad(gy, gb)
-        return gx, gw, gb, None
+        return (_first_order(gx, gy, weight), _first_order(gw, gy, x2), _first_order(gb, gy),
+                None)
 
 
 class Linear8bitLt(torch.nn.Module):

@@ -44,3 +44,30 @@ def test_tangents_of_parameters_are_refused(monkeypatch, which):
         setattr(m, which, fwAD.make_dual(p, torch.ones_like(p)))
         with pytest.raises(NotImplementedError, match="forward-mode"):
             m(x)
+
+
+@pytest.mark.parametrize("fp16_weights", [True, False])
+def test_second_derivatives_are_refused(monkeypatch, fp16_weights):
+    m = _layer(monkeypatch, fp16_weights)
+    x = torch.ones((T, K), dtype=H, requires_grad=True)
+    if fp16_weights:
+        for of, to in ((x, m.weight), (m.weight, x)):      # each gradient depends on the other operand
+            first, = torch.autograd.grad(m(x).float().sum(), of, create_graph=True)
+            with pytest.raises(NotImplementedError, match="second"):
+                torch.autograd.grad(first.float().square().sum() + to.float().square().sum(), to)
+        first, = torch.autograd.grad(m(x).float().sum(), m.bias, create_graph=True)
+        assert not first.requires_grad
+    y = m(x)
+    gy = torch.ones_like(y).requires_grad_(True)
+    first, = torch.autograd.grad(y, x, gy, create_graph=True)
+    with pytest.raises(NotImplementedError, match="second"):
+        torch.autograd.grad(first.float().square().sum() + gy.float().square().sum(), gy)
+
+
+def test_create_graph_gives_the_same_gradients(monkeypatch):
+    m = _layer(monkeypatch, True)
+    x = torch.ones((T, K), dtype=H, requires_grad=True)
+    wanted = (x, m.weight, m.bias)
+    for a, b in zip(torch.autograd.grad(m(x).float().sum(), wanted),
+                    torch.autograd.grad(m(x).float().sum(), wanted, create_graph=True)):
+        assert torch.equal(a, b)

@@ -37,7 +37,7 @@ from typing import Dict, Iterable, Optional
 import torch
 
 from . import abi
-from .block import _first_order, _no_tangent
+from .block import FixedTypes, _first_order, _no_tangent
 
 
 class _Int8LinearFn(torch.autograd.Function):
@@ -87,7 +87,7 @@ class _Int8LinearFn(torch.autograd.Function):
                 None)
 
 
-class Linear8bitLt(torch.nn.Module):
+class Linear8bitLt(FixedTypes):
     """y = x W^T + b computed as the LLM.int8() decomposition of x (fp16) and W.
 
     Buffers (saved and restored by ``state_dict``): ``CB`` int8 [out, in] (the weight's
@@ -101,7 +101,11 @@ class Linear8bitLt(torch.nn.Module):
     ``outlier_cache_cols``: capacity (columns) of the outlier cache, 0 = no cache.  The cache
     is not part of the state dict; ``quantize_`` and ``load_state_dict`` empty it, as they
     rewrite CB in place (write CB through neither, and call ``invalidate_outlier_cache``).
+
+    A cast of the model leaves the types of CB and SCB alone.
     """
+
+    FIXED = ("CB", "SCB")
 
     def __init__(self, in_features: int, out_features: int, bias: bool = True,
                  threshold: float = 6.0, device=None, has_fp16_weights: bool = False,

@@ -71,3 +71,17 @@ def test_create_graph_gives_the_same_gradients(monkeypatch):
     for a, b in zip(torch.autograd.grad(m(x).float().sum(), wanted),
                     torch.autograd.grad(m(x).float().sum(), wanted, create_graph=True)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("cast", [lambda m: m.half(), lambda m: m.to(torch.bfloat16), lambda m: m.half().float(),
+                                  lambda m: m.type(torch.float16)])
+@pytest.mark.parametrize("fp16_weights,code_format", [(False, "int8"), (False, "e4m3"), (True, "int8")])
+def test_casts_leave_codes_and_scales(cast, fp16_weights, code_format):
+    g = torch.Generator().manual_seed(2)
+    m = linear.Linear8bitLt(K, N, has_fp16_weights=fp16_weights, code_format=code_format)
+    m.CB.copy_(torch.randint(0, 127, (N, K), generator=g))
+    m.SCB.copy_(torch.rand(N, generator=g))
+    codes, scales = m.CB.clone(), m.SCB.clone()
+    m = cast(torch.nn.Sequential(m))[0]
+    assert m.CB.dtype == codes.dtype and torch.equal(m.CB, codes)
+    assert m.SCB.dtype == torch.float32 and torch.equal(m.SCB, scales)

@@ -50,6 +50,8 @@ def _dense(t: torch.Tensor) -> torch.Tensor:
 def _no_tangent(*tensors):
     """Refuses forward-mode dual tensors: a library call fills a fresh buffer, which would have
     no tangent, and so a derivative of zero."""
+    if forward_ad._current_level < 0:       # no dual_level() is open: no dual tensor (1 us saved)
+        return
     for t in tensors:
         if t is not None and forward_ad.unpack_dual(t).tangent is not None:
             raise NotImplementedError("no forward-mode derivative: the library's layers have "
@@ -68,13 +70,14 @@ class _FirstOrder(torch.autograd.Function):
 
 
 def _first_order(grad, *depends):
-    """A gradient on its way out of a backward that the library computed.  Under create_graph it
-    is tied to the tensors of the graph that it depends on, so that differentiating it again
-    raises; without the tie its terms would be missing from the sum and no error seen.
-    (torch.autograd.function.once_differentiable ties it to the gradients that came in alone: a
-    constant one, as sum() gives, leaves nothing to raise.)"""
-    if grad is None or not torch.is_grad_enabled():
-        return grad
+    """A gradient on its way out of a backward that the library computed, under create_graph (the
+    only time that gradients are enabled in a backward).  It is tied to the tensors of the graph
+    that it depends on, so that differentiating it again raises; without the tie its terms would
+    be missing from the sum and no error seen.  (torch.autograd.function.once_differentiable ties
+    it to the gradients that came in alone: a constant one, as sum() gives, leaves nothing to
+    raise.)"""
+    if grad is None:
+        return None
     depends = [t for t in depends if t is not None and t.requires_grad]
     return _FirstOrder.apply(grad, *depends) if depends else grad
 
@@ -154,7 +157,9 @@ class _BlockLinearFn(torch.autograd.Function):
         codes, scales = ctx.saved_tensors
         gx, _, gb = _backward(gy, None, codes, scales, codes.shape[1], ctx.needs_input_grad[0],
                               False, ctx.needs_input_grad[3], ctx.dtype)
-        return _first_order(gx, gy), None, None, _first_order(gb, gy)
+        if torch.is_grad_enabled():
+            gx, gb = _first_order(gx, gy), _first_order(gb, gy)
+        return gx, None, None, gb
 
 
 class _BlockLinearTrainFn(torch.autograd.Function):
@@ -172,8 +177,9 @@ class _BlockLinearTrainFn(torch.autograd.Function):
         x2, codes, scales = ctx.saved_tensors
         gx, gw, gb = _backward(gy, x2, codes, scales, codes.shape[1], *ctx.needs_input_grad[:3],
                                x2.dtype)
-        return (_first_order(gx, gy, ctx.tie), _first_order(gw, gy, x2), _first_order(gb, gy),
-                None)
+        if torch.is_grad_enabled():
+            gx, gw, gb = _first_order(gx, gy, ctx.tie), _first_order(gw, gy, x2), _first_order(gb, gy)
+        return gx, gw, gb, None
 
 
 def linear_block_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,

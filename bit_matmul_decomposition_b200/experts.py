@@ -48,7 +48,9 @@ class _RouteFn(torch.autograd.Function):
         if logits.shape[0] > 0:
             with _on(logits.device):
                 abi.i8_route_experts_backward(logits, *ctx.how, idx, _dense(gw), gl)
-        return (_first_order(gl, gw, logits),) + (None,) * 7
+        if torch.is_grad_enabled():
+            gl = _first_order(gl, gw, logits)
+        return (gl,) + (None,) * 7
 
 
 def route_experts(logits: torch.Tensor, top_k: int, balance: Optional[torch.Tensor] = None, *,
@@ -125,7 +127,9 @@ class _ExpertsFn(torch.autograd.Function):
                                 dtype=torch.uint8)
             with _on(gy.device):
                 abi.i8_experts_backward(gy, idx, w, CB13, S13, CB2, S2, gu, gx, gw, ws)
-        return (_first_order(gx, gy, ctx.tie, w), _first_order(gw, gy, ctx.tie)) + (None,) * 6
+        if torch.is_grad_enabled():
+            gx, gw = _first_order(gx, gy, ctx.tie, w), _first_order(gw, gy, ctx.tie)
+        return (gx, gw) + (None,) * 6
 
 
 def experts_block_fp8(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor,

@@ -83,8 +83,9 @@ class _Int8LinearFn(torch.autograd.Function):
             if want_b:
                 gb = torch.empty((N,), dtype=torch.float16, device=dev)
                 abi.i8_bias_grad(gy, gb)
-        return (_first_order(gx, gy, weight), _first_order(gw, gy, x2), _first_order(gb, gy),
-                None)
+        if torch.is_grad_enabled():
+            gx, gw, gb = _first_order(gx, gy, weight), _first_order(gw, gy, x2), _first_order(gb, gy)
+        return gx, gw, gb, None
 
 
 class Linear8bitLt(FixedTypes):

@@ -33,7 +33,8 @@
 // each CTA's 128 rows of B being 64 rows of the gate weight and the same 64 of the up weight,
 // so that a thread ends with g and u of the same 64 features of its row.  h = silu(g) * u is
 // formed in fp32, the row's maximum over the 128 features joined between the two threads that
-// hold it, and h leaves as e4m3 row codes and scales: neither g, u nor h goes through memory.
+// hold it, and h leaves as e4m3 row codes and scales.  g and u go to memory (fp32) only for a
+// backward that will read them.
 #pragma once
 
 #include "block_quant.cuh"
@@ -168,8 +169,9 @@ __device__ __forceinline__ void bulk_wait_read_0() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
-// sigmoid(g) for silu(g) = g * sigmoid(g), within a few units in the last place of fp32.  For g
-// below about -88, exp(-g) is infinite and the sigmoid 0: g * 0 = -0, the limit.
+// sigmoid(g) for silu(g) = g * sigmoid(g), within a few units in the last place of fp32.  Below g =
+// -87.3, where the sigmoid is smaller than 2^-126, it comes out as 0 (the quick division gives 0
+// for divisors above 2^126, an infinite exp(-g) among them): g * 0 = -0, the limit.
 __device__ __forceinline__ float fast_sigmoid(float g) { return __fdividef(1.0f, 1.0f + expf(-g)); }
 
 // 64 bytes a thread (16 fp32 or 32 16-bit columns of its row) of a warp's 32 rows through 2 KB of

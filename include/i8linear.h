@@ -439,6 +439,10 @@ i8_status i8_route_experts_backward(const void* logits, int32_t dtype, int64_t T
  *   dh = q(dY) W2;  dweights[t,j] = sum_i dh_i h_i;  dX = sum_j ( q(dg) W1 + q(du) W3 ) with
  *   dg, du the gradients of h = silu(g) * u times weights[t,j].  dX [T, K] in dtype, dweights
  *   [T, k] fp32 (0 for a choice without an expert).  idx and weights as in the forward.
+ *   dweights takes the coded dY and h itself: straight through the coding of h, from the product
+ *   that dX needs anyway.  dY times the coded h's rows, which Y is linear in, differs from it by
+ *   the rounding of the codes (3 to 4 in 100 on random data; from the uncoded product it is off by
+ *   2, dweights by 2 to 3) and would need the rows of W2's product kept or formed again.
  * workspace: at least i8_experts_workspace_size / i8_experts_backward_workspace_size bytes.
  */
 size_t i8_experts_workspace_size(int64_t T, int64_t K, int64_t I, int64_t E, int64_t k);

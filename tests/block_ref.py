@@ -152,8 +152,7 @@ def route_grad(P, idx, dw, score, renormalize, scale):
 
 # ------------------------------------------------------------------ experts
 def experts(x, idx, w, W1, W3, W2, dy=None):
-    """y, and with dy also dx and dw; W1, W3 [E][I, K] and W2 [E][K, I] in 64 bits.  The bounds
-    returned beside them are of the fp32 arithmetic (see experts_bound)."""
+    """y, and with dy also dx and dw; W1, W3 [E][I, K] and W2 [E][K, I] in 64 bits."""
     T, K = x.shape
     xq = rows_value(x)
     y, dx = torch.zeros(T, K, dtype=torch.float64), torch.zeros(T, K, dtype=torch.float64)

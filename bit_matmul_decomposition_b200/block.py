@@ -185,7 +185,8 @@ class _BlockLinearTrainFn(torch.autograd.Function):
 def linear_block_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
                      bias: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y = x W^T + bias with W given as e4m3 codes [N, K] (uint8 or float8_e4m3fn) and scales
-    [ceil(N/128), ceil(K/128)].  x: fp16 or bf16 [..., K], bias: x's type [N]."""
+    [ceil(N/128), ceil(K/128)].  x: fp16 or bf16 [..., K], bias: x's type [N].  Differentiable in x
+    and bias; codes and scales are constants."""
     if codes.dim() != 2:
         raise ValueError("codes: a 2-D tensor is required")
     _check_input(x, codes.shape[1], codes.device)
@@ -215,8 +216,8 @@ def linear_block_fp8_train(x: torch.Tensor, weight: torch.Tensor,
 
 class FixedTypes(torch.nn.Module):
     """A module some of whose tensors have the one type that the library takes: casts of the
-    model (``.half()``, ``.to(torch.bfloat16)``, ``.double()``) move them, but leave type and values
-    alone.  Cast, the scales would lose bits for good, and fp16 holds few of them at all."""
+    model (``.half()``, ``.to(torch.bfloat16)``, ``.double()``) move them, but leave type, values and
+    layout alone.  Cast, the scales would lose bits for good, and fp16 holds few of them at all."""
 
     FIXED: Tuple[str, ...] = ()                # names of such buffers and parameters
 
@@ -229,7 +230,7 @@ class FixedTypes(torch.nn.Module):
 
         def keep(t):
             out = fn(t)
-            if out.dtype != t.dtype and any(t is f for f in fixed):
+            if any(t is f for f in fixed) and (out.dtype != t.dtype or not out.is_contiguous()):
                 return t.detach().to(out.device)
             return out
 

@@ -88,3 +88,13 @@ def test_router_logits_stay_fp32_under_autocast(monkeypatch, dtype):
     assert seen["logits"].dtype == torch.float32 and torch.equal(seen["logits"], plain)
     seen["logits"].sum().backward()
     assert torch.equal(r.gate.grad, x.float().sum(0).expand(3, 144))
+
+
+def test_a_memory_format_leaves_the_layout():
+    """channels_last reorders 4-D tensors; the library takes codes and scales row by row."""
+    m = _layer("experts")
+    before = {n: t.clone() for n, t in m[0].state_dict().items()}
+    for fmt in (torch.channels_last, torch.contiguous_format):
+        m = m.to(torch.float16, memory_format=fmt)
+        for n, t in m[0].state_dict().items():
+            assert t.is_contiguous() and t.dtype == before[n].dtype and torch.equal(t, before[n]), n

@@ -236,6 +236,20 @@ class FixedTypes(torch.nn.Module):
 
         return super()._apply(keep, recurse=False)
 
+    def _load_from_state_dict(self, state_dict, prefix, metadata, strict, missing, unexpected, errors):
+        for name in self.FIXED:
+            own, t = getattr(self, name, None), state_dict.get(prefix + name)
+            if own is None or own.dtype != torch.uint8 or not isinstance(t, torch.Tensor):
+                continue
+            # stored as float8_e4m3fn the codes are taken as they are, not converted as numbers
+            if t.dtype == torch.float8_e4m3fn:
+                state_dict[prefix + name] = t.view(torch.uint8)
+            elif t.is_floating_point() and t.element_size() == 1:
+                errors.append("%s%s: codes of type %s, expected uint8 or float8_e4m3fn"
+                              % (prefix, name, t.dtype))
+        super()._load_from_state_dict(state_dict, prefix, metadata, strict, missing, unexpected,
+                                      errors)
+
 
 class LinearBlockFp8(FixedTypes):
     """nn.Linear with a block-scaled e4m3 weight.

@@ -98,3 +98,29 @@ def test_a_memory_format_leaves_the_layout():
         m = m.to(torch.float16, memory_format=fmt)
         for n, t in m[0].state_dict().items():
             assert t.is_contiguous() and t.dtype == before[n].dtype and torch.equal(t, before[n]), n
+
+
+@pytest.mark.parametrize("assign", [False, True])
+@pytest.mark.parametrize("kind", ["frozen", "experts", "routed"])
+def test_stored_float8_codes_load_as_codes(kind, assign):
+    """A checkpoint's codes are float8_e4m3fn; copied into bytes as numbers, 1.5 would become 1."""
+    m = _layer(kind)[0]
+    state = m.state_dict()
+    stored = {n: t.view(torch.float8_e4m3fn) if t.dtype == torch.uint8 else t.clone() for n, t in state.items()}
+    want = {n: t.clone() for n, t in state.items()}
+    fresh = _layer(kind)[0]
+    for b in fresh.buffers():
+        b.zero_()
+    fresh.load_state_dict(stored, assign=assign)
+    for n, t in fresh.state_dict().items():
+        assert t.dtype == want[n].dtype and torch.equal(t, want[n]), n
+    assert any(t.dtype == torch.float8_e4m3fn for t in stored.values())    # the caller's stay as they were
+
+
+@pytest.mark.parametrize("dtype", [torch.float8_e5m2, torch.float8_e4m3fnuz])
+def test_other_8_bit_floats_do_not_load(dtype):
+    m = _layer("frozen")[0]
+    state = dict(m.state_dict())
+    state["CB"] = torch.zeros(state["CB"].shape).to(dtype)
+    with pytest.raises(RuntimeError, match="float8_e4m3fn"):
+        m.load_state_dict(state)
